@@ -286,7 +286,7 @@ def _plain_tables(st):
     start = end - count
     bad = (lens < 0) | (new < 0)
     long = ~bad & (lens + new > W * P)
-    over = ~bad & ~long & (end > room)
+    over = ~bad & ~long & (count > 0) & (end > room)
     fits = ~(bad | long | over)
     have = (lens.clamp(min=0) + P - 1) // P
     need = torch.where(fits, (lens + new + P - 1) // P - have, 0)
