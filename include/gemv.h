@@ -407,6 +407,11 @@ int gemv_workspace_release(void);
  * for a NULL pointer, or GEMV_ERR_CUDA.
  */
 #define GEMV_STATUS_WAIT_TIMEOUT 1u
+/* GEMV_STATUS_BAD_PAGE: gemv_attn_decode met a page number outside the pool, a
+ * length past its row of the table, or a query row out of range. Nothing is
+ * read through it: those tokens count as masked, that length is cut, that
+ * request is skipped. */
+#define GEMV_STATUS_BAD_PAGE 2u
 int gemv_device_status(unsigned int *bits, int reset);
 
 /*
@@ -514,6 +519,234 @@ int gemv_fp8_query_launch(int64_t N, int64_t K, int B, int sm_count,
  */
 int gemv_probe_stream_read(const void *src, int64_t bytes, float *sink, void *stream);
 int gemv_probe_sink_words(void);
+
+/*
+ * The attention half of a decode step: what stands between the QKV projection
+ * and o_proj. gemv_block_tables gives every new token of a batch its page and
+ * slot, gemv_rope_append turns q and k by their positions and writes k and v
+ * into the paged cache at those slots, gemv_attn_decode attends from one new
+ * token of each request to its pages. The rules above hold: asynchronous on
+ * the stream, arguments checked before anything is launched, nothing
+ * allocated, results the same from call to call. The calls run on the current
+ * device, which must be the stream's and the tensors'. They may be captured;
+ * the argument records are read during the call only, the arrays they name
+ * when the kernels run. A first call on a device sets the library up there and
+ * must come before any capture.
+ *
+ * A paged cache: num_pages pages of page_size slots, each slot one token's
+ * kv_heads rows of head_dim values (a multiple of 8; of 16 for FP8; at most
+ * GEMV_MAX_HEAD_DIM), one pool for k and one of the same layout for v. Value d
+ * of head h in slot s of page g is element
+ *     g * page_stride + h * head_stride + s * slot_stride + d
+ * so both usual orders ([pages][slots][heads][dim] and
+ * [pages][heads][slots][dim]) and parts of a larger pool are strides. Strides
+ * count elements and are multiples of 16 bytes; k and v are 16-byte aligned;
+ * num_pages * page_size <= 2^31 - 1. Slot number g * page_size + s names slot
+ * s of page g. What a slot holds that no length reaches is never part of a sum
+ * (it may be NaN).
+ *   GEMV_CACHE_BF16: BF16 values; the scales are NULL.
+ *   GEMV_CACHE_FP8:  E4M3 codes; a value is its code times k_scale[h] or
+ *                    v_scale[h] (FP32, kv_heads each; NULL: 1).
+ */
+#define GEMV_CACHE_BF16 0
+#define GEMV_CACHE_FP8 1
+#define GEMV_MAX_HEAD_DIM 256
+
+typedef struct {
+    void *k;
+    void *v;
+    int64_t page_stride;
+    int64_t head_stride;
+    int64_t slot_stride;
+    const float *k_scale;
+    const float *v_scale;
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t kind;
+} gemv_kv_cache;
+
+/*
+ * Block tables and slot maps from request lengths, on the device. Request r
+ * holds lens[r] tokens and gets new_tokens[r] more (0: none this step). Its
+ * pages are table[r * table_stride + b], b < ceil(lens[r] / page_size); new
+ * ones are taken, in request order, from free_pages[*free_next ..] (free_cap
+ * entries). With the new tokens numbered through the batch (request 0's first):
+ *   token_start[r]  number of r's first new token; token_start[requests] their
+ *                   count (both at most 2^31 - 1);
+ *   page_start[r]   index in free_pages of r's first new page, -1 if refused;
+ *   table           the new pages' entries are written, no other;
+ *   slots[t], positions[t], t < max_tokens: slot number (page * page_size +
+ *                   place) and position (lens[r] + i) of token t; slot -1 and
+ *                   position 0 for tokens of refused requests and behind the
+ *                   last token, slot -1 where the page number is not below
+ *                   num_pages;
+ *   new_lens[r]     lens[r] + new_tokens[r]; lens[r] if refused;
+ *   status[r]       0, or why r was refused: 1 the free list ran out (it and
+ *                   every later request that needs a page), 2 longer than its
+ *                   row of table_width entries, 3 its tokens end past
+ *                   max_tokens, 4 a negative length or count. A refused request
+ *                   takes no pages; its tokens keep their numbers;
+ *   free_next_out   *free_next plus the pages taken.
+ * new_lens may be lens and free_next_out may be free_next, so that a captured
+ * call advances its own state; otherwise no output overlaps anything else.
+ * max_tokens >= 1; table_width * page_size and num_pages * page_size at most
+ * 2^31 - 1. All arrays are int32, 4-byte aligned.
+ */
+typedef struct {
+    const int32_t *lens;
+    const int32_t *new_tokens;
+    const int32_t *free_pages;
+    const int32_t *free_next;
+    int32_t *table;
+    int32_t *slots;
+    int32_t *positions;
+    int32_t *token_start;
+    int32_t *page_start;
+    int32_t *new_lens;
+    int32_t *status;
+    int32_t *free_next_out;
+    int64_t table_stride;
+    int64_t max_tokens;
+    int32_t requests;
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t table_width;
+    int32_t free_cap;
+} gemv_block_tables_args;
+
+int gemv_block_tables(const gemv_block_tables_args *args, void *stream);
+
+/*
+ * Rotary positions. Pair i < rot_dim / 2 of a head is columns (i, i +
+ * rot_dim / 2) with GEMV_PAIRS_HALF, (2i, 2i + 1) with GEMV_PAIRS_INTERLEAVED;
+ * it is turned by the angle
+ *     positions[axis * axis_stride + t] * inv_freq[i],  axis = pair_axis[i]
+ * (columns from rot_dim on are copied). With one axis pair_axis is unused and
+ * may be NULL; images and video give each pair one of up to GEMV_MAX_AXES axes
+ * (time, height, width). freqs holds inv_freq as gemv_rope_freqs makes it: the
+ * angle is then reduced exactly however far the position is.
+ *   q: rows of q_heads x head_dim values, k and v of kv_heads x head_dim, FP32
+ *      (the projections' outputs) or BF16 (GEMV_ROWS_*), row strides in
+ *      elements; head_dim and rot_dim are even. Turned in FP32, rounded once.
+ *   q_out: BF16 rows of the same shape, stride q_out_stride.
+ * tokens = 0 is allowed and does nothing.
+ *
+ * gemv_rope: k goes to k_out (BF16 rows, stride k_out_stride); v and slots are
+ * NULL. q_out may be q and k_out may be k where those are BF16 with the same
+ * stride.
+ *
+ * gemv_rope_append: k and v go to the cache, token t to slots[t]; k_out is
+ * NULL, kv_heads and head_dim are the cache's. A token whose slot is negative
+ * or not in the pool is padding: neither its q_out row nor anything in the
+ * cache is written. Slots that are in the pool must differ from each other.
+ * FP8: the code nearest to value / scale, at most 448 in magnitude (infinities
+ * too; NaN stays NaN).
+ */
+#define GEMV_ROWS_F32 0
+#define GEMV_ROWS_BF16 1
+#define GEMV_PAIRS_HALF 0
+#define GEMV_PAIRS_INTERLEAVED 1
+#define GEMV_MAX_AXES 8
+
+typedef struct {
+    const void *q;
+    const void *k;
+    const void *v;
+    void *q_out;
+    void *k_out;
+    const int32_t *positions;
+    const int64_t *freqs;
+    const int32_t *pair_axis;
+    const int32_t *slots;
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    int64_t q_out_stride;
+    int64_t k_out_stride;
+    int64_t axis_stride;
+    int32_t tokens;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t rot_dim;
+    int32_t rows;
+    int32_t pairs;
+    int32_t axes;
+} gemv_rope_args;
+
+int gemv_rope(const gemv_rope_args *args, void *stream);
+int gemv_rope_append(const gemv_rope_args *args, const gemv_kv_cache *cache, void *stream);
+
+/* inv_freq[i] (radians per position, finite) as a 64-bit fraction of a turn:
+ * inv_freq / (2 pi) modulo 1, in units of 2^-64. Both arrays of n values are in
+ * host memory; the caller copies freqs to the device once. */
+int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
+
+/*
+ * Attention of one new token per request over its pages: with j over the
+ * visible tokens of request r,
+ *     s_j = scale * q . k_j           (softcap > 0: softcap * tanh(s_j / softcap))
+ *     out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
+ * Visible are the tokens j < lens[r] (the new one included, its k and v already
+ * in the cache), with window > 0 only the last window of them. Query head i
+ * reads key-value head i / (q_heads / kv_heads).
+ *   q, out: BF16 rows of q_heads x head_dim values, strides in elements
+ *           (multiples of 4), 8-byte aligned;  lse: [row][q_heads] FP32 or NULL.
+ *   token_start NULL: request r's query is row r. Else (gemv_block_tables'
+ *           array, requests + 1 entries) it is row token_start[r + 1] - 1, the
+ *           last of its new tokens; a request without new tokens is skipped.
+ *           rows: rows that q and out have (read with token_start only).
+ *   table:  page numbers, table_width per request, as gemv_block_tables leaves
+ *           them; entries past a request's last page are not read.
+ * A request of length 0 gets zeros and lse -inf, as does one whose visible
+ * tokens all lie in pages outside the pool (GEMV_STATUS_BAD_PAGE); one of
+ * negative length is skipped, its rows left as they were.
+ *   workspace: gemv_attn_query's bytes, 16-byte aligned, zeroed once before its
+ *           first use (every call leaves it fit for the next, of any shape that
+ *           needs no more bytes). Calls that may run at the same time need a
+ *           workspace each, replayed graphs among them.
+ * Products of BF16 (FP8: codes widened exactly to FP16, and q scaled into FP16
+ * by a power of two per head) are summed in FP32, the softmax is kept in FP32;
+ * the probabilities meet V as two BF16 parts (FP8: as FP16). requests = 0 is
+ * allowed and does nothing. More than 1,024 query heads per key-value head:
+ * GEMV_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *lens;
+    const int32_t *token_start;
+    const int32_t *table;
+    void *workspace;
+    int64_t q_stride;
+    int64_t out_stride;
+    int64_t table_stride;
+    int64_t rows;
+    int32_t requests;
+    int32_t q_heads;
+    int32_t table_width;
+    int32_t window;
+    float scale;
+    float softcap;
+} gemv_attn_args;
+
+int gemv_attn_decode(const gemv_attn_args *args, const gemv_kv_cache *cache, void *stream);
+
+/* How a head layout is launched, and the workspace its calls need. Host
+ * arithmetic; kind is GEMV_CACHE_*, sm_count the GPU's SM count. */
+typedef struct {
+    int64_t workspace_bytes;
+    int32_t grid;            /* CTAs (whole sets of head_tiles)                  */
+    int32_t warps_per_cta;
+    int32_t head_tile;       /* query heads one CTA carries                      */
+    int32_t head_tiles;      /* CTAs that share the heads of a key-value head    */
+    int32_t dim_tile;        /* head size the kernel instance is built for       */
+} gemv_attn_info;
+
+int gemv_attn_query(int q_heads, int kv_heads, int head_dim, int kind, int sm_count, gemv_attn_info *out);
 
 /* Human-readable name of a status code. Never NULL. */
 const char *gemv_status_string(int status);

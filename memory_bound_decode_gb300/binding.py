@@ -47,6 +47,7 @@ EXPORTED = [
     "gemv_debug_write_count",
     "gemv_w4_bf16", "gemv_w4_query_launch", "gemv_fp8_bf16", "gemv_fp8_query_launch",
     "gemv_probe_stream_read", "gemv_probe_sink_words",
+    "gemv_block_tables", "gemv_rope", "gemv_rope_append", "gemv_rope_freqs", "gemv_attn_decode", "gemv_attn_query",
     "gemv_status_string", "gemv_last_cuda_error",
 ]
 
@@ -78,6 +79,54 @@ class gemv_launch_info(ctypes.Structure):
                 ("dp_rounds", ctypes.c_int32), ("mcast", ctypes.c_int32), ("xbox", ctypes.c_int32),
                 ("xpieces", ctypes.c_int32), ("xboxes_per_piece", ctypes.c_int32), ("persistent", ctypes.c_int32),
                 ("l2_prefetch", ctypes.c_int32)]
+
+    def as_dict(self) -> dict:
+        return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+GEMV_CACHE_BF16 = 0
+GEMV_CACHE_FP8 = 1
+GEMV_MAX_HEAD_DIM = 256
+GEMV_ROWS_F32 = 0
+GEMV_ROWS_BF16 = 1
+GEMV_PAIRS_HALF = 0
+GEMV_PAIRS_INTERLEAVED = 1
+GEMV_MAX_AXES = 8
+
+i32 = ctypes.c_int32
+
+
+class gemv_kv_cache(ctypes.Structure):
+    _fields_ = ([(n, vp) for n in ("k", "v")] + [(n, i64) for n in ("page_stride", "head_stride", "slot_stride")]
+                + [(n, vp) for n in ("k_scale", "v_scale")]
+                + [(n, i32) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "kind")])
+
+
+class gemv_block_tables_args(ctypes.Structure):
+    _fields_ = ([(n, vp) for n in ("lens", "new_tokens", "free_pages", "free_next", "table", "slots", "positions",
+                                   "token_start", "page_start", "new_lens", "status", "free_next_out")]
+                + [(n, i64) for n in ("table_stride", "max_tokens")]
+                + [(n, i32) for n in ("requests", "page_size", "num_pages", "table_width", "free_cap")])
+
+
+class gemv_rope_args(ctypes.Structure):
+    _fields_ = ([(n, vp) for n in ("q", "k", "v", "q_out", "k_out", "positions", "freqs", "pair_axis", "slots")]
+                + [(n, i64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride",
+                                      "axis_stride")]
+                + [(n, i32) for n in ("tokens", "q_heads", "kv_heads", "head_dim", "rot_dim", "rows", "pairs",
+                                      "axes")])
+
+
+class gemv_attn_args(ctypes.Structure):
+    _fields_ = ([(n, vp) for n in ("q", "out", "lse", "lens", "token_start", "table", "workspace")]
+                + [(n, i64) for n in ("q_stride", "out_stride", "table_stride", "rows")]
+                + [(n, i32) for n in ("requests", "q_heads", "table_width", "window")]
+                + [("scale", ctypes.c_float), ("softcap", ctypes.c_float)])
+
+
+class gemv_attn_info(ctypes.Structure):
+    _fields_ = [("workspace_bytes", i64)] + [(n, i32) for n in ("grid", "warps_per_cta", "head_tile", "head_tiles",
+                                                                "dim_tile")]
 
     def as_dict(self) -> dict:
         return {name: getattr(self, name) for name, _ in self._fields_}
@@ -166,6 +215,12 @@ def _load(path: str) -> ctypes.CDLL:
                                         ctypes.POINTER(gemv_launch_info)]
     L.gemv_probe_stream_read.argtypes = [vp, i64, vp, vp]
     L.gemv_probe_sink_words.argtypes = []
+    L.gemv_block_tables.argtypes = [ctypes.POINTER(gemv_block_tables_args), vp]
+    L.gemv_rope.argtypes = [ctypes.POINTER(gemv_rope_args), vp]
+    L.gemv_rope_append.argtypes = [ctypes.POINTER(gemv_rope_args), ctypes.POINTER(gemv_kv_cache), vp]
+    L.gemv_rope_freqs.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.c_int, ctypes.POINTER(i64)]
+    L.gemv_attn_decode.argtypes = [ctypes.POINTER(gemv_attn_args), ctypes.POINTER(gemv_kv_cache), vp]
+    L.gemv_attn_query.argtypes = [ctypes.c_int] * 5 + [ctypes.POINTER(gemv_attn_info)]
     L.gemv_status_string.argtypes = [ctypes.c_int]
     L.gemv_status_string.restype = ctypes.c_char_p
     L.gemv_last_cuda_error.argtypes = []
@@ -302,6 +357,7 @@ def gemv_workspace_release() -> int:
 
 
 GEMV_STATUS_WAIT_TIMEOUT = 1
+GEMV_STATUS_BAD_PAGE = 2
 
 
 def gemv_device_status(reset: bool = True) -> int:
@@ -346,6 +402,115 @@ def gemv_probe_sink_words() -> int:
 def gemv_probe_stream_read(src, nbytes: int, sink, stream=None) -> int:
     return _check(lib().gemv_probe_stream_read(_ptr(src), nbytes, _ptr(sink), _stream(stream)),
                   "gemv_probe_stream_read")
+
+
+# ---- the attention half of a decode step ----------------------------------------
+#
+# The calls take the C structures. The functions without the gemv_ prefix fill
+# them from tensors (or addresses) and keep the tensors referenced; a structure
+# is filled once and used for every step, as its arrays are updated in place.
+
+def _record(cls, pointers: dict, numbers: dict):
+    rec = cls(**{n: _ptr(t) for n, t in pointers.items()}, **numbers)
+    rec.keepalive = list(pointers.values())
+    return rec
+
+
+def kv_cache(k, v, *, num_pages: int, page_size: int, kv_heads: int, head_dim: int, page_stride: int,
+             head_stride: int, slot_stride: int, kind: int = GEMV_CACHE_BF16, k_scale=None,
+             v_scale=None) -> gemv_kv_cache:
+    """A paged cache (see gemv.h); strides in elements."""
+    return _record(gemv_kv_cache, dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale),
+                   dict(num_pages=num_pages, page_size=page_size, kv_heads=kv_heads, head_dim=head_dim,
+                        page_stride=page_stride, head_stride=head_stride, slot_stride=slot_stride, kind=kind))
+
+
+def block_tables_args(*, lens, new_tokens, requests: int, page_size: int, num_pages: int, table, table_width: int,
+                      table_stride: int, free_pages, free_cap: int, free_next, max_tokens: int, slots, positions,
+                      token_start, page_start, new_lens, status, free_next_out) -> gemv_block_tables_args:
+    return _record(gemv_block_tables_args,
+                   dict(lens=lens, new_tokens=new_tokens, free_pages=free_pages, free_next=free_next, table=table,
+                        slots=slots, positions=positions, token_start=token_start, page_start=page_start,
+                        new_lens=new_lens, status=status, free_next_out=free_next_out),
+                   dict(table_stride=table_stride, max_tokens=max_tokens, requests=requests, page_size=page_size,
+                        num_pages=num_pages, table_width=table_width, free_cap=free_cap))
+
+
+def rope_args(*, q, k, q_out, positions, freqs, tokens: int, q_heads: int, kv_heads: int, head_dim: int, rot_dim: int,
+              q_stride: int, k_stride: int, q_out_stride: int, v=None, v_stride: int = 0, k_out=None,
+              k_out_stride: int = 0, slots=None, rows: int = GEMV_ROWS_F32, pairs: int = GEMV_PAIRS_HALF,
+              axes: int = 1, axis_stride: int = 0, pair_axis=None) -> gemv_rope_args:
+    return _record(gemv_rope_args,
+                   dict(q=q, k=k, v=v, q_out=q_out, k_out=k_out, positions=positions, freqs=freqs,
+                        pair_axis=pair_axis, slots=slots),
+                   dict(q_stride=q_stride, k_stride=k_stride, v_stride=v_stride, q_out_stride=q_out_stride,
+                        k_out_stride=k_out_stride, axis_stride=axis_stride, tokens=tokens, q_heads=q_heads,
+                        kv_heads=kv_heads, head_dim=head_dim, rot_dim=rot_dim, rows=rows, pairs=pairs, axes=axes))
+
+
+def attn_args(*, q, out, lens, requests: int, q_heads: int, q_stride: int, out_stride: int, table, table_width: int,
+              table_stride: int, scale: float, workspace, lse=None, token_start=None, rows: int = 0,
+              softcap: float = 0.0, window: int = 0) -> gemv_attn_args:
+    return _record(gemv_attn_args,
+                   dict(q=q, out=out, lse=lse, lens=lens, token_start=token_start, table=table, workspace=workspace),
+                   dict(q_stride=q_stride, out_stride=out_stride, table_stride=table_stride, rows=rows,
+                        requests=requests, q_heads=q_heads, table_width=table_width, window=window, scale=scale,
+                        softcap=softcap))
+
+
+def gemv_block_tables(args: gemv_block_tables_args, stream=None, check: bool = True) -> int:
+    """Pages, slots and positions of a step's new tokens (see gemv.h)."""
+    rc = lib().gemv_block_tables(ctypes.byref(args), _stream(stream))
+    return _check(rc, "gemv_block_tables") if check else rc
+
+
+def gemv_rope(args: gemv_rope_args, stream=None, check: bool = True) -> int:
+    """q and k turned by their positions (see gemv.h)."""
+    rc = lib().gemv_rope(ctypes.byref(args), _stream(stream))
+    return _check(rc, "gemv_rope") if check else rc
+
+
+def gemv_rope_append(args: gemv_rope_args, cache: gemv_kv_cache, stream=None, check: bool = True) -> int:
+    """gemv_rope with k and v written into the paged cache (see gemv.h)."""
+    rc = lib().gemv_rope_append(ctypes.byref(args), ctypes.byref(cache), _stream(stream))
+    return _check(rc, "gemv_rope_append") if check else rc
+
+
+def gemv_rope_freqs(inv_freq) -> list[int]:
+    """inv_freq (radians per position) as 64-bit fractions of a turn."""
+    n = len(inv_freq)
+    src, dst = (ctypes.c_double * max(1, n))(*inv_freq), (i64 * max(1, n))()
+    _check(lib().gemv_rope_freqs(src, n, dst), "gemv_rope_freqs")
+    return list(dst[:n])
+
+
+def rope_freqs(inv_freq, device=None):
+    """gemv_rope_freqs as an int64 tensor on ``device`` (default: inv_freq's own)."""
+    import torch
+    if isinstance(inv_freq, torch.Tensor):
+        device = inv_freq.device if device is None else device
+        inv_freq = inv_freq.tolist()
+    return torch.tensor(gemv_rope_freqs(inv_freq), dtype=torch.int64, device=device)
+
+
+def gemv_attn_decode(args: gemv_attn_args, cache: gemv_kv_cache, stream=None, check: bool = True) -> int:
+    """Attention of one new token per request over its pages (see gemv.h)."""
+    rc = lib().gemv_attn_decode(ctypes.byref(args), ctypes.byref(cache), _stream(stream))
+    return _check(rc, "gemv_attn_decode") if check else rc
+
+
+def gemv_attn_query(q_heads: int, kv_heads: int, head_dim: int, kind: int, sm_count: int) -> dict:
+    info = gemv_attn_info()
+    _check(lib().gemv_attn_query(q_heads, kv_heads, head_dim, kind, sm_count, ctypes.byref(info)), "gemv_attn_query")
+    return info.as_dict()
+
+
+def attn_workspace(q_heads: int, kv_heads: int, head_dim: int, kind: int = GEMV_CACHE_BF16, device="cuda"):
+    """A zeroed workspace for gemv_attn_decode calls of this head layout."""
+    import torch
+    sms = torch.cuda.get_device_properties(device).multi_processor_count
+    n = gemv_attn_query(q_heads, kv_heads, head_dim, kind, sms)["workspace_bytes"]
+    return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 class Plan:

@@ -34,12 +34,23 @@ SOURCES = [
     "gemv_streamk_instances.cu",
     "gemv_noalloc.cu",
     "gemv_dispatch.cu",
+    "gemv_attn_bf16_64.cu",
+    "gemv_attn_bf16_128.cu",
+    "gemv_attn_bf16_256.cu",
+    "gemv_attn_fp8_64.cu",
+    "gemv_attn_fp8_128.cu",
+    "gemv_attn_fp8_256.cu",
+    "gemv_attn_dispatch.cu",
+    "gemv_rope.cu",
+    "gemv_blocks.cu",
     "planner.cpp",
     "gemv_api.cpp",
+    "gemv_attn_api.cpp",
 ]
 HEADERS = ["gemv_internal.h", "gemv_common.cuh", "gemv_kernel.cuh", "gemv_mma_kernel.cuh", "gemv_w4_kernel.cuh",
            "gemv_tc_kernel.cuh",
-           "gemv_streamk_kernel.cuh", "gemv_fp8_kernel.cuh", os.path.join("..", "..", "include", "gemv.h")]
+           "gemv_streamk_kernel.cuh", "gemv_fp8_kernel.cuh", "gemv_attn_internal.h", "gemv_attn_kernel.cuh",
+           "gemv_attn_instances.cuh", os.path.join("..", "..", "include", "gemv.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/gemv.h"
+#include "gemv_attn_internal.h"
 #include "gemv_internal.h"
 
 using gemv::Launch;
@@ -77,7 +78,7 @@ int device_state(int* sm_count) {
             return cuda_fail(e);
         if (major != 10 || minor != 3) {
             st.status = GEMV_ERR_UNSUPPORTED;
-        } else if ((e = gemv::prepare_kernels(dev)) != cudaSuccess) {
+        } else if ((e = gemv::prepare_kernels(dev)) != cudaSuccess || (e = gemv::prepare_attn()) != cudaSuccess) {
             return cuda_fail(e);
         } else {
             st.status = GEMV_OK;
@@ -617,6 +618,14 @@ bool plan_is_independent(const gemv_proj* projs, int nproj, const std::vector<si
 
 }  // namespace
 
+namespace gemv {
+
+int api_device_state(int* sm_count) { return device_state(sm_count); }
+int api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+bool api_pdl_enabled() { return pdl_enabled(); }
+
+}  // namespace gemv
+
 extern "C" {
 
 int gemv_bf16_ex(const void* W, const void* x, float* y, int64_t N, int64_t K, int B, int64_t ldw,
@@ -1141,14 +1150,15 @@ int gemv_device_status(unsigned int* bits, int reset) {
     if (!bits) return GEMV_ERR_INVALID;
     *bits = 0;
     // Each kernel translation unit keeps its own status word.
-    unsigned int b1 = 0, b2 = 0, b3 = 0, b4 = 0, b5 = 0;
+    unsigned int b1 = 0, b2 = 0, b3 = 0, b4 = 0, b5 = 0, b6 = 0;
     cudaError_t e = gemv::read_fma_status(&b1, reset != 0);
     if (e == cudaSuccess) e = gemv::read_mma_status_nb1(&b2, reset != 0);
     if (e == cudaSuccess) e = gemv::read_mma_status_nb2(&b3, reset != 0);
     if (e == cudaSuccess) e = gemv::read_fp8_status(&b4, reset != 0);
     if (e == cudaSuccess) e = gemv::read_tc_status(&b5, reset != 0);
+    if (e == cudaSuccess) e = gemv::read_attn_status(&b6, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e);
-    *bits = b1 | b2 | b3 | b4 | b5;
+    *bits = b1 | b2 | b3 | b4 | b5 | b6;
     return GEMV_OK;
 }
 

@@ -1,0 +1,293 @@
+// C-ABI front end of the decode step's attention half: argument checks and
+// launches of the block tables, the rotary positions with the cache write, and
+// the paged decode attention.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "../../include/gemv.h"
+#include "gemv_attn_internal.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Whether a pool of n items `stride` bytes apart stays within 2^60 bytes, so
+// that the kernels' 64-bit offsets cannot wrap.
+bool fits(int64_t n, int64_t stride) { return n <= 1 || stride <= (int64_t(1) << 60) / n; }
+
+int check_cache(const gemv_kv_cache* c) {
+    if (!c || !c->k || !c->v) return GEMV_ERR_INVALID;
+    if (c->kind != GEMV_CACHE_BF16 && c->kind != GEMV_CACHE_FP8) return GEMV_ERR_INVALID;
+    if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->kv_heads > 4096) return GEMV_ERR_INVALID;
+    if (static_cast<int64_t>(c->num_pages) * c->page_size > 0x7fffffffLL) return GEMV_ERR_INVALID;
+    const int unit = c->kind == GEMV_CACHE_FP8 ? 16 : 8;      // elements of a 16-byte access
+    if (c->head_dim < unit || c->head_dim > GEMV_MAX_HEAD_DIM || c->head_dim % unit != 0) return GEMV_ERR_INVALID;
+    const int64_t d = c->head_dim;
+    if ((c->num_pages > 1 && c->page_stride < d) || (c->kv_heads > 1 && c->head_stride < d) ||
+        (c->page_size > 1 && c->slot_stride < d) || c->page_stride < 0 || c->head_stride < 0 || c->slot_stride < 0)
+        return GEMV_ERR_INVALID;
+    if (!fits(c->num_pages, 2 * c->page_stride) || !fits(c->kv_heads, 2 * c->head_stride) ||
+        !fits(c->page_size, 2 * c->slot_stride) || c->page_stride > (int64_t(1) << 59))
+        return GEMV_ERR_INVALID;
+    if (c->kind == GEMV_CACHE_BF16 && (c->k_scale || c->v_scale)) return GEMV_ERR_INVALID;
+    if (c->page_stride % unit != 0 || c->head_stride % unit != 0 || c->slot_stride % unit != 0 || !aligned(c->k, 16) ||
+        !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return GEMV_ERR_ALIGN;
+    return GEMV_OK;
+}
+
+int elem_bytes(const gemv_kv_cache* c) { return c->kind == GEMV_CACHE_FP8 ? 1 : 2; }
+
+int check_rope(const gemv_rope_args* a) {
+    if (!a || !a->q || !a->k || !a->q_out || !a->positions || !a->freqs) return GEMV_ERR_INVALID;
+    if (a->tokens < 0 || a->q_heads < 1 || a->q_heads > 4096 || a->kv_heads < 1 || a->kv_heads > 4096)
+        return GEMV_ERR_INVALID;
+    if (a->head_dim < 2 || a->head_dim > GEMV_MAX_HEAD_DIM || a->head_dim % 2 != 0) return GEMV_ERR_INVALID;
+    if (a->rot_dim < 2 || a->rot_dim > a->head_dim || a->rot_dim % 2 != 0) return GEMV_ERR_INVALID;
+    if (a->rows != GEMV_ROWS_F32 && a->rows != GEMV_ROWS_BF16) return GEMV_ERR_INVALID;
+    if (a->pairs != GEMV_PAIRS_HALF && a->pairs != GEMV_PAIRS_INTERLEAVED) return GEMV_ERR_INVALID;
+    if (a->axes < 1 || a->axes > GEMV_MAX_AXES || (a->axes > 1 && (!a->pair_axis || a->axis_stride < a->tokens)))
+        return GEMV_ERR_INVALID;
+    const int64_t qw = static_cast<int64_t>(a->q_heads) * a->head_dim;
+    const int64_t kw = static_cast<int64_t>(a->kv_heads) * a->head_dim;
+    if (a->q_stride < qw || a->k_stride < kw || a->q_out_stride < qw || (a->v && a->v_stride < kw))
+        return GEMV_ERR_INVALID;
+    const int64_t most = int64_t(1) << 40;                     // times 2^31 tokens at most
+    if (a->q_stride > most || a->k_stride > most || a->q_out_stride > most || (a->v && a->v_stride > most) ||
+        a->axis_stride > most)
+        return GEMV_ERR_INVALID;
+    const uintptr_t es = a->rows == GEMV_ROWS_F32 ? 4 : 2;
+    if (!aligned(a->q, es) || !aligned(a->k, es) || !aligned(a->v, es) || !aligned(a->q_out, 2) ||
+        !aligned(a->positions, 4) || !aligned(a->freqs, 8) || !aligned(a->pair_axis, 4))
+        return GEMV_ERR_ALIGN;
+    return GEMV_OK;
+}
+
+// What both rotary calls hand to the kernel.
+void fill_rope(const gemv_rope_args* a, gemv::RopeParams* p) {
+    p->q = a->q;
+    p->k = a->k;
+    p->positions = a->positions;
+    p->freqs = a->freqs;
+    p->pair_axis = a->axes > 1 ? a->pair_axis : nullptr;
+    p->q_out = static_cast<uint16_t*>(a->q_out);
+    p->q_stride = a->q_stride;
+    p->k_stride = a->k_stride;
+    p->v_stride = a->v_stride;
+    p->q_out_stride = a->q_out_stride;
+    p->axis_stride = a->axis_stride;
+    p->tokens = a->tokens;
+    p->q_heads = a->q_heads;
+    p->kv_heads = a->kv_heads;
+    p->head_dim = a->head_dim;
+    p->rot_dim = a->rot_dim;
+    p->rows_f32 = a->rows == GEMV_ROWS_F32;
+    p->interleaved = a->pairs == GEMV_PAIRS_INTERLEAVED;
+    p->axes = a->axes;
+    // Four pairs at a time where every such group is whole and starts on the boundary of its vector access.
+    const uintptr_t in = p->rows_f32 ? 16 : 8;
+    p->vec = a->head_dim % 8 == 0 && a->rot_dim % 8 == 0 && a->q_stride % 4 == 0 && a->k_stride % 4 == 0 &&
+             a->q_out_stride % 4 == 0 && aligned(a->q, in) && aligned(a->k, in) && aligned(a->q_out, 8) &&
+             (!a->v || (a->v_stride % 4 == 0 && aligned(a->v, in)));
+}
+
+int finish(cudaError_t e) { return e == cudaSuccess ? GEMV_OK : gemv::api_cuda_fail(e); }
+
+}  // namespace
+
+extern "C" {
+
+int gemv_block_tables(const gemv_block_tables_args* a, void* stream) {
+    if (!a || !a->lens || !a->new_tokens || !a->free_next || !a->table || !a->slots || !a->positions ||
+        !a->token_start || !a->page_start || !a->new_lens || !a->status || !a->free_next_out)
+        return GEMV_ERR_INVALID;
+    if (a->requests < 1 || a->page_size < 1 || a->num_pages < 1 || a->table_width < 1 || a->free_cap < 0 ||
+        (a->free_cap > 0 && !a->free_pages))
+        return GEMV_ERR_INVALID;
+    if (static_cast<int64_t>(a->num_pages) * a->page_size > 0x7fffffffLL ||
+        static_cast<int64_t>(a->table_width) * a->page_size > 0x7fffffffLL)
+        return GEMV_ERR_INVALID;
+    if (a->max_tokens < 1 || a->max_tokens > 0x7fffffffLL || a->table_stride < a->table_width ||
+        a->table_stride > (int64_t(1) << 31))
+        return GEMV_ERR_INVALID;
+    const void* all[] = {a->lens, a->new_tokens, a->free_pages, a->free_next, a->table, a->slots, a->positions,
+                         a->token_start, a->page_start, a->new_lens, a->status, a->free_next_out};
+    for (const void* q : all)
+        if (!aligned(q, 4)) return GEMV_ERR_ALIGN;
+    int sm_count = 0;
+    const int rc = gemv::api_device_state(&sm_count);
+    if (rc != GEMV_OK) return rc;
+    gemv::TablesParams p = {};
+    p.lens = a->lens;
+    p.new_tokens = a->new_tokens;
+    p.free_pages = a->free_pages;
+    p.free_next = a->free_next;
+    p.table = a->table;
+    p.slots = a->slots;
+    p.positions = a->positions;
+    p.token_start = a->token_start;
+    p.page_start = a->page_start;
+    p.new_lens = a->new_lens;
+    p.status = a->status;
+    p.free_next_out = a->free_next_out;
+    p.table_stride = a->table_stride;
+    p.max_tokens = a->max_tokens;
+    p.requests = a->requests;
+    p.page_size = a->page_size;
+    p.num_pages = a->num_pages;
+    p.table_width = a->table_width;
+    p.free_cap = a->free_cap;
+    return finish(gemv::launch_tables(p, sm_count, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
+}
+
+int gemv_rope_freqs(const double* inv_freq, int n, int64_t* freqs) {
+    if (!inv_freq || !freqs || n < 1) return GEMV_ERR_INVALID;
+    for (int i = 0; i < n; ++i)
+        if (!std::isfinite(inv_freq[i])) return GEMV_ERR_INVALID;
+    for (int i = 0; i < n; ++i) {
+        // The fraction of a turn in [0, 1), as a multiple of 2^-64 (what rounds up to a whole turn wraps to 0).
+        const double turns = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
+        const double part = turns - std::floor(turns);
+        const double high = std::floor(std::ldexp(part, 32));
+        const double low = std::floor(std::ldexp(std::ldexp(part, 32) - high, 32));
+        freqs[i] = static_cast<int64_t>((static_cast<uint64_t>(high) << 32) + static_cast<uint64_t>(low));
+    }
+    return GEMV_OK;
+}
+
+int gemv_rope(const gemv_rope_args* a, void* stream) {
+    int rc = check_rope(a);
+    if (rc != GEMV_OK) return rc;
+    if (!a->k_out || a->v || a->slots) return GEMV_ERR_INVALID;
+    if (a->k_out_stride < static_cast<int64_t>(a->kv_heads) * a->head_dim || a->k_out_stride > (int64_t(1) << 40))
+        return GEMV_ERR_INVALID;
+    if (!aligned(a->k_out, 2)) return GEMV_ERR_ALIGN;
+    if (a->tokens == 0) return GEMV_OK;
+    int sm_count = 0;
+    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
+    gemv::RopeParams p = {};
+    fill_rope(a, &p);
+    p.vec = p.vec && a->k_out_stride % 4 == 0 && aligned(a->k_out, 8);
+    // k_out as a cache of pages of one token
+    p.kc = static_cast<unsigned char*>(a->k_out);
+    p.page_size = 1;
+    p.page_stride = a->k_out_stride * 2;
+    p.head_stride = a->head_dim * 2;
+    p.num_slots = a->tokens;
+    return finish(gemv::launch_rope(p, sm_count, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
+}
+
+int gemv_rope_append(const gemv_rope_args* a, const gemv_kv_cache* c, void* stream) {
+    int rc = check_rope(a);
+    if (rc != GEMV_OK) return rc;
+    if ((rc = check_cache(c)) != GEMV_OK) return rc;
+    if (!a->v || !a->slots || a->k_out) return GEMV_ERR_INVALID;
+    if (a->kv_heads != c->kv_heads || a->head_dim != c->head_dim) return GEMV_ERR_INVALID;
+    if (!aligned(a->slots, 4)) return GEMV_ERR_ALIGN;
+    if (a->tokens == 0) return GEMV_OK;
+    int sm_count = 0;
+    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
+    gemv::RopeParams p = {};
+    fill_rope(a, &p);
+    p.v = a->v;
+    p.slots = a->slots;
+    p.kc = static_cast<unsigned char*>(c->k);
+    p.vc = static_cast<unsigned char*>(c->v);
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.fp8 = c->kind == GEMV_CACHE_FP8;
+    p.page_size = c->page_size;
+    const int es = elem_bytes(c);
+    p.page_stride = c->page_stride * es;
+    p.head_stride = c->head_stride * es;
+    p.slot_stride = c->slot_stride * es;
+    p.num_slots = static_cast<int64_t>(c->num_pages) * c->page_size;
+    return finish(gemv::launch_rope(p, sm_count, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
+}
+
+int gemv_attn_query(int q_heads, int kv_heads, int head_dim, int kind, int sm_count, gemv_attn_info* out) {
+    if (!out || sm_count < 1 || kv_heads < 1 || kv_heads > 4096 || q_heads < kv_heads || q_heads % kv_heads != 0)
+        return GEMV_ERR_INVALID;
+    if (kind != GEMV_CACHE_BF16 && kind != GEMV_CACHE_FP8) return GEMV_ERR_INVALID;
+    const int unit = kind == GEMV_CACHE_FP8 ? 16 : 8;
+    if (head_dim < unit || head_dim > GEMV_MAX_HEAD_DIM || head_dim % unit != 0) return GEMV_ERR_INVALID;
+    if (q_heads / kv_heads > gemv::kAttnMaxGroup) return GEMV_ERR_UNSUPPORTED;
+    gemv::AttnLaunch l = {};
+    const int rc = gemv::plan_attn(q_heads, kv_heads, head_dim, kind == GEMV_CACHE_FP8, sm_count, &l);
+    if (rc != GEMV_OK) return rc;
+    out->workspace_bytes = l.workspace_bytes;
+    out->grid = l.grid;
+    out->warps_per_cta = l.warps;
+    out->head_tile = l.nb * 8;
+    out->head_tiles = l.qtiles;
+    out->dim_tile = l.dt;
+    return GEMV_OK;
+}
+
+int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stream) {
+    if (!a || !a->q || !a->out || !a->lens || !a->table || !a->workspace) return GEMV_ERR_INVALID;
+    int rc = check_cache(c);
+    if (rc != GEMV_OK) return rc;
+    if (a->requests < 0 || a->q_heads < c->kv_heads || a->q_heads % c->kv_heads != 0) return GEMV_ERR_INVALID;
+    const int group = a->q_heads / c->kv_heads;
+    if (group > gemv::kAttnMaxGroup) return GEMV_ERR_UNSUPPORTED;
+    const int64_t width = static_cast<int64_t>(a->q_heads) * c->head_dim;
+    const int64_t most = int64_t(1) << 31;
+    if (a->q_stride < width || a->out_stride < width || a->q_stride > most || a->out_stride > most)
+        return GEMV_ERR_INVALID;
+    if (a->table_width < 1 || a->table_stride < a->table_width || a->table_stride > most) return GEMV_ERR_INVALID;
+    if (!std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0.f || a->window < 0)
+        return GEMV_ERR_INVALID;
+    if (a->token_start && (a->rows < 0 || a->rows > 0x7fffffffLL)) return GEMV_ERR_INVALID;
+    if (a->q_stride % 4 != 0 || a->out_stride % 4 != 0 || !aligned(a->q, 8) || !aligned(a->out, 8) ||
+        !aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(a->table, 4) || !aligned(a->token_start, 4) ||
+        !aligned(a->workspace, 16))
+        return GEMV_ERR_ALIGN;
+    if (a->requests == 0) return GEMV_OK;
+    int sm_count = 0;
+    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
+    gemv::AttnLaunch l = {};
+    const int fp8 = c->kind == GEMV_CACHE_FP8;
+    if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, fp8, sm_count, &l)) != GEMV_OK) return rc;
+    gemv::AttnParams p = {};
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.out = static_cast<uint16_t*>(a->out);
+    p.lse = a->lse;
+    p.lens = a->lens;
+    p.token_start = a->token_start;
+    p.rows = a->rows;
+    p.table = a->table;
+    p.kc = static_cast<const unsigned char*>(c->k);
+    p.vc = static_cast<const unsigned char*>(c->v);
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    char* ws = static_cast<char*>(a->workspace);
+    p.ticket = reinterpret_cast<uint32_t*>(ws);
+    p.part = reinterpret_cast<float*>(ws + gemv::kAttnTickets * 4);
+    p.part_ml = p.part + static_cast<int64_t>(l.grid) * 2 * l.nb * 8 * l.dt;
+    p.q_stride = a->q_stride;
+    p.out_stride = a->out_stride;
+    p.table_stride = a->table_stride;
+    p.page_stride = c->page_stride * elem_bytes(c);
+    p.head_stride = c->head_stride * elem_bytes(c);
+    p.slot_stride = c->slot_stride * elem_bytes(c);
+    p.requests = a->requests;
+    p.q_heads = a->q_heads;
+    p.kv_heads = c->kv_heads;
+    p.group = group;
+    p.qtiles = l.qtiles;
+    p.head_dim = c->head_dim;
+    p.page_size = c->page_size;
+    p.table_width = a->table_width;
+    p.num_pages = c->num_pages;
+    p.window = a->window;
+    const int64_t reach = static_cast<int64_t>(a->table_width) * c->page_size;
+    p.max_len = static_cast<int32_t>(reach < 0x7fffffe0LL ? reach : 0x7fffffe0LL);
+    p.scale = a->scale;
+    p.softcap = a->softcap;
+    return finish(gemv::launch_attn(p, l, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
+}
+
+}  // extern "C"

@@ -1,0 +1,106 @@
+// Internal declarations of the decode step's attention half: block tables,
+// rotary positions with the cache write, paged decode attention. Shared by
+// their kernels and the C-ABI front end; the public interface is
+// include/gemv.h.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace gemv {
+
+// ---- shared with gemv_api.cpp -------------------------------------------------
+int api_device_state(int* sm_count);      // set-up of the current device; GEMV_OK or an error
+int api_cuda_fail(cudaError_t e);         // record e for gemv_last_cuda_error; GEMV_ERR_CUDA
+bool api_pdl_enabled();
+
+// ---- attention ----------------------------------------------------------------
+
+constexpr int kAttnSlice = 16;            // tokens a warp takes at a time (one MMA tile)
+constexpr int kAttnTickets = 1024;        // join counters at the start of the workspace
+constexpr int kAttnMaxGroup = 1024;       // query heads per key-value head
+
+struct AttnParams {
+    const uint16_t* q;          // BF16
+    uint16_t* out;              // BF16
+    float* lse;
+    const int32_t* lens;
+    const int32_t* token_start; // null: request r's query is row r
+    const int32_t* table;
+    const unsigned char* kc;
+    const unsigned char* vc;
+    const float* k_scale;
+    const float* v_scale;
+    float* part;                // partial outputs of rows cut between CTAs
+    float* part_ml;             // their maxima and sums
+    uint32_t* ticket;
+    int64_t q_stride, out_stride, table_stride;
+    int64_t page_stride, head_stride, slot_stride;   // bytes
+    int64_t rows;               // rows of q and out
+    int32_t requests, q_heads, kv_heads, group, qtiles;
+    int32_t head_dim, page_size, table_width, num_pages, window, max_len;
+    float scale, softcap;
+};
+
+struct AttnLaunch {
+    int dt;            // head size the instance is built for: 64, 128 or 256
+    int nb;            // blocks of 8 query heads a CTA carries
+    int fp8;
+    int warps, stages, smem_bytes;
+    int qtiles, grid;
+    int64_t workspace_bytes;
+};
+
+int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, AttnLaunch* l);
+
+cudaError_t launch_attn(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl);
+cudaError_t prepare_attn();
+cudaError_t read_attn_status(unsigned int* bits, bool reset);
+
+// ---- rotary positions -----------------------------------------------------------
+
+struct RopeParams {
+    const void* q;
+    const void* k;
+    const void* v;              // null: no v
+    const int32_t* positions;
+    const int64_t* freqs;
+    const int32_t* pair_axis;   // null: axis 0
+    const int32_t* slots;       // null: k goes to row t of kc
+    uint16_t* q_out;
+    unsigned char* kc;          // the cache, or k_out
+    unsigned char* vc;
+    const float* k_scale;
+    const float* v_scale;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;   // elements
+    int64_t axis_stride;
+    int64_t page_stride, head_stride, slot_stride;        // bytes
+    int64_t num_slots;
+    int32_t tokens, q_heads, kv_heads, head_dim, rot_dim, page_size;
+    int32_t rows_f32, interleaved, fp8, axes, vec;
+};
+
+cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t s, bool pdl);
+
+// ---- block tables ---------------------------------------------------------------
+
+struct TablesParams {
+    const int32_t* lens;
+    const int32_t* new_tokens;
+    const int32_t* free_pages;
+    const int32_t* free_next;
+    int32_t* table;
+    int32_t* slots;
+    int32_t* positions;
+    int32_t* token_start;
+    int32_t* page_start;
+    int32_t* new_lens;
+    int32_t* status;
+    int32_t* free_next_out;
+    int64_t table_stride, max_tokens;
+    int32_t requests, page_size, num_pages, table_width, free_cap;
+};
+
+cudaError_t launch_tables(const TablesParams& p, int sm_count, cudaStream_t s, bool pdl);
+
+}  // namespace gemv

@@ -1,0 +1,256 @@
+"""gemv_attn_decode against the definition in 64 bits, through the C ABI."""
+import math
+
+import pytest
+import torch
+
+from memory_bound_decode_gb300 import binding
+from tests import attn_util as au
+
+pytestmark = pytest.mark.gpu
+
+
+def run(lens, q_heads, heads, dim, page, kind="bf16", layout="token", **kw):
+    extra = kw.pop("extra", 0)
+    cache = au.Cache(lens, page, heads, dim, kind, layout, seed=len(lens) + page + dim, extra=extra)
+    a = au.Attn(lens, cache, q_heads, **kw)
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
+    assert binding.gemv_device_status() == 0
+    return a
+
+
+EDGES = [0, 1, 2, 15, 16, 17, 31, 33, 0, 127, 128, 129]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("layout", ["token", "head"])
+@pytest.mark.parametrize("page", [1, 7, 16, 24, 128])
+def test_edges_of_length_and_page(kind, layout, page):
+    run(EDGES, 8, 2, 64, page, kind, layout)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 128, 144, 192, 256])
+def test_head_sizes(kind, dim):
+    run([5, 300, 0, 64, 1000], 8, 2, dim, 16, kind)
+
+
+@pytest.mark.parametrize("dim", [8, 72, 120, 248])
+def test_head_sizes_of_eight(dim):
+    run([5, 300, 0, 64], 4, 2, dim, 16)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 2, 5, 8, 9, 16, 17, 32, 33, 71])
+def test_groups(kind, dim, group):
+    run([1, 100, 513], group * 2, 2, dim, 16, kind, "head")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens", [[1], [40], [5000], [20011], [20000] * 3, list(range(300)), [1] * 700])
+def test_splits(kind, lens):
+    """One row over many CTAs, many rows in one CTA, more requests than threads."""
+    run(lens, 4, 1, 128, 32, kind, "head")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("window", [1, 2, 16, 17, 100, 5000])
+def test_window(kind, window):
+    run([0, 1, 2, 16, 17, 99, 100, 101, 116, 117, 3001], 8, 2, 128, 24, kind, window=window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_softcap_and_scale(kind):
+    run([1, 77, 1024], 8, 2, 64, 16, kind, softcap=5.0)
+    run([1, 77, 1024], 8, 2, 64, 16, kind, softcap=30.0, window=50, scale=0.5)
+    run([1, 77, 1024], 8, 2, 64, 16, kind, scale=-0.25)
+    run([1, 77, 1024], 8, 2, 64, 16, kind, scale=0.0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_strides(kind):
+    """Pages inside a larger pool, rows of q and out apart, no lse."""
+    run([40, 0, 333], 8, 2, 80, 16, kind, extra=16 * 5, pad=12, lse=False)
+
+
+def test_queries_by_token_start_and_skipped_requests():
+    """Request r's query is the last of its new tokens; requests without any, or of negative length, are left."""
+    lens = [50, 7, 300, 0, 64, -1, 20]
+    starts = [0, 3, 3, 4, 6, 6, 7, 8]
+    cache = au.Cache(lens, 16, 2, 64, seed=3)
+    a = au.Attn(lens, cache, 8, token_start=starts, rows=10)
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
+    a = au.Attn(lens, cache, 8)     # a row per request: the negative length's is left
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
+
+
+def test_token_start_out_of_range_is_skipped():
+    lens = [50, 60]
+    cache = au.Cache(lens, 16, 2, 64, seed=3)
+    a = au.Attn(lens, cache, 8, token_start=[0, 1, 9], rows=2)
+    binding.gemv_device_status()
+    a.run()
+    torch.cuda.synchronize()
+    assert binding.gemv_device_status() == binding.GEMV_STATUS_BAD_PAGE
+    mark = float(torch.tensor(-777.0).bfloat16())
+    assert (a.out[1].float() == mark).all() and (a.out[0].float() != mark).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_pages_outside_the_pool_count_as_masked(kind):
+    lens = [64, 40]
+    cache = au.Cache(lens, 16, 2, 64, kind, seed=5)
+    bad = cache.table.clone()
+    bad[0, 1], bad[1, :] = cache.num_pages, -1
+    a = au.Attn(lens, cache, 8, table=bad)
+    binding.gemv_device_status()
+    a.run()
+    torch.cuda.synchronize()
+    assert binding.gemv_device_status() == binding.GEMV_STATUS_BAD_PAGE
+    assert (a.out[1].float() == 0).all() and (a.lse[1] == -math.inf).all()
+    keep = [i for i in range(64) if not 16 <= i < 32]
+    k, v = (cache.values[i][0][keep] for i in range(2))
+    out, z, mass, size = au.attend(a.q[0].cpu().view(8, 64), k, v, a.scale)
+    tol, tol_z = au.attn_bounds(out, z, mass, size, 64, 64, kind)
+    assert ((a.out[0].double().cpu().view(8, 64) - out).abs() <= tol).all()
+    assert ((a.lse[0].double().cpu() - z).abs() <= tol_z).all()
+
+
+def test_length_past_the_table_is_cut():
+    cache = au.Cache([48], 16, 2, 64, seed=5)
+    a = au.Attn([100], cache, 8)
+    binding.gemv_device_status()
+    a.run()
+    torch.cuda.synchronize()
+    assert binding.gemv_device_status() == binding.GEMV_STATUS_BAD_PAGE
+    a.check(lens=[48])
+
+
+def test_peaked_scores_and_late_maximum():
+    """Scores that differ by far more than the exponent's range, the largest first or last."""
+    n, D = 700, 64
+    for where in (0, 350, n - 1):
+        cache = au.Cache([n], 16, 1, D, seed=9)
+        q = torch.zeros(1, 4, D, dtype=torch.bfloat16)
+        q[..., 0] = 100.0
+        vk = cache.view(0)
+        for j in range(n):
+            val = 60.0 if j == where else -float(j % 50)
+            vk[int(cache.table[0, j // 16]), j % 16, 0, 0] = val
+            cache.values[0][0][j, 0, 0] = float(torch.tensor(val).bfloat16())
+        a = au.Attn([n], cache, 4, q=q.cuda(), scale=1.0)
+        a.run()
+        torch.cuda.synchronize()
+        a.check()
+
+
+def test_infinite_and_nan_keys():
+    """A NaN key makes its heads NaN, as the definition does; other requests are untouched."""
+    lens = [40, 40]
+    cache = au.Cache(lens, 16, 2, 64, seed=5)
+    cache.view(0)[int(cache.table[0, 1]), 3, 1, 5] = float("nan")
+    a = au.Attn(lens, cache, 8)
+    a.run()
+    torch.cuda.synchronize()
+    o = a.out.float().view(2, 8, 64)
+    assert torch.isnan(o[0, 4:]).all() and torch.isnan(a.lse[0, 4:]).all()
+    assert torch.isfinite(o[0, :4]).all() and torch.isfinite(o[1]).all()
+    cache = au.Cache(lens, 16, 2, 64, seed=5)
+    a = au.Attn(lens, cache, 8)
+    cache.view(0)[int(cache.table[0, 1]), 3, 1, 5] = -math.inf * torch.sign(a.q[0, 4 * 64 + 5]).item()
+    a.run()
+    torch.cuda.synchronize()
+    o = a.out.float().view(2, 8, 64)
+    assert torch.isfinite(o[0, 4]).all()      # score -inf: that token has no weight
+
+
+def test_same_bits_every_time_and_workspace_left_ready():
+    lens = [9000, 3, 0, 4097, 811]
+    cache = au.Cache(lens, 16, 2, 128, seed=2)
+    a = au.Attn(lens, cache, 16)
+    outs = []
+    for _ in range(4):
+        a.run()
+        torch.cuda.synchronize()
+        outs.append((a.out.clone(), a.lse.clone()))
+    for o, z in outs[1:]:
+        assert torch.equal(o.view(torch.int16), outs[0][0].view(torch.int16)) and torch.equal(z, outs[0][1])
+    a.check()
+    assert (a.ws[:4096] == 0).all()
+    other = au.Cache([5000, 200], 24, 1, 64, seed=4)      # another shape on the same workspace
+    b = au.Attn([5000, 200], other, 4, workspace=a.ws)
+    b.run()
+    torch.cuda.synchronize()
+    b.check()
+
+
+def test_two_streams_with_a_workspace_each():
+    jobs = []
+    for i in range(4):
+        lens = [3000 + 17 * i, 5, 900]
+        cache = au.Cache(lens, 16, 2, 64, seed=i)
+        jobs.append((au.Attn(lens, cache, 8, seed=i), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for a, s in jobs:
+            a.run(s)
+    torch.cuda.synchronize()
+    for a, _ in jobs:
+        a.check()
+
+
+def test_captured_and_replayed_with_new_lengths():
+    lens = [700, 3, 64, 1]
+    cache = au.Cache(lens, 16, 2, 64, seed=8)
+    a = au.Attn(lens, cache, 8)
+    a.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run()
+    for new in ([700, 3, 64, 1], [1, 0, 33, 0], [699, 2, 50, 1]):
+        a.lens_t.copy_(torch.tensor(new, dtype=torch.int32))
+        a.guard.fill_(-777.0)
+        a.lse.fill_(-777.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        a.check(lens=new)
+
+
+def test_offsets_past_32_bits():
+    """Pages that begin past 2^32 bytes, and past 2^31 elements of the pool."""
+    page, heads, dim = 16, 2, 64
+    stride = 1 << 27                              # elements from page to page: 20 pages, 5.4 GB
+    n, pages = 300, 20
+    pool = torch.empty(pages * stride, dtype=torch.bfloat16, device="cuda")
+    view = torch.as_strided(pool, (pages, page, heads, dim), (stride, heads * dim, dim, 1))
+    rows = au.randn(1, pages, page, heads, dim, dtype=torch.bfloat16)
+    view.copy_(rows)
+    small = au.Cache([n], page, heads, dim, seed=1)
+    small.num_pages, small.page_stride, small.width = pages, stride, pages
+    order = torch.arange(pages - 1, -1, -1, dtype=torch.int32)
+    small.table = order[None].cuda()
+    small.pools = [pool, pool]
+    vals = rows.cpu().double()[order.long()].reshape(-1, heads, dim)[:n]
+    small.values = [[vals], [vals]]
+    a = au.Attn([n], small, 8)
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
+
+
+def test_no_requests():
+    cache = au.Cache([4], 16, 2, 64)
+    a = au.Attn([4], cache, 8)
+    a.args.requests = 0
+    a.run()
+    torch.cuda.synchronize()
+    mark = float(torch.tensor(-777.0).bfloat16())
+    assert (a.guard.float() == mark).all()
