@@ -13,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import sys
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -241,8 +242,10 @@ def _ptr(t) -> int | None:
 
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        torch = sys.modules.get("torch")     # not imported, or without a context: no stream but the default one
+        if torch is None or not torch.cuda.is_initialized():
+            return None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())   # a tenth of current_stream()'s time
     if isinstance(s, int):
         return s
     return s.cuda_stream

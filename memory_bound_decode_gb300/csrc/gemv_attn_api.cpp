@@ -3,6 +3,7 @@
 // the paged decode attention.
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include <cuda_runtime.h>
 
@@ -285,6 +286,12 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.window = a->window;
     const int64_t reach = static_cast<int64_t>(a->table_width) * c->page_size;
     p.max_len = static_cast<int32_t>(reach < 0x7fffffe0LL ? reach : 0x7fffffe0LL);
+    p.page_shift = -1;
+    if ((c->page_size & (c->page_size - 1)) == 0)
+        for (p.page_shift = 0; (1 << p.page_shift) < c->page_size; ++p.page_shift) {
+        }
+    p.min_slices = 8;
+    if (const char* v = std::getenv("GEMV_ATTN_MIN")) p.min_slices = atoi(v);
     p.scale = a->scale;
     p.softcap = a->softcap;
     return finish(gemv::launch_attn(p, l, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));

@@ -34,7 +34,7 @@ int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, At
     if (l->grid > kAttnTickets) return GEMV_ERR_UNSUPPORTED;
     const int64_t heads = static_cast<int64_t>(l->grid) * 2 * l->nb * 8;   // two pieces per CTA
     l->workspace_bytes = kAttnTickets * 4 + heads * (2 + l->dt) * 4;
-    l->warps = l->dt == 256 ? 4 : 8;
+    l->warps = 8;
     return GEMV_OK;
 }
 

@@ -6,40 +6,25 @@
 
 namespace gemv {
 
-// Warps and slices in flight per instance: the ring takes about 192 KB of the
-// SM's 227 KB, one CTA per SM.
-template <int DT, bool FP8>
-struct AttnTune {
-    static constexpr int kWarps = DT == 256 ? 4 : 8;
-    static constexpr int kStages = (DT == 64 ? 6 : 3) * (FP8 && DT > 64 ? 2 : 1);
-};
-
-template <int DT, int NB, bool FP8>
-int attn_smem() {
-    return AttnShape<DT, NB, FP8, AttnTune<DT, FP8>::kWarps, AttnTune<DT, FP8>::kStages>::kSmem;
-}
-
 template <int DT, int NB, bool FP8>
 cudaError_t attn_prepare_one() {
-    return cudaFuncSetAttribute(
-        attn_decode_kernel<DT, NB, FP8, AttnTune<DT, FP8>::kWarps, AttnTune<DT, FP8>::kStages>,
-        cudaFuncAttributeMaxDynamicSharedMemorySize, attn_smem<DT, NB, FP8>());
+    return cudaFuncSetAttribute(attn_decode_kernel<DT, NB, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                AttnShape<DT, NB, FP8>::kSmem);
 }
 
 template <int DT, int NB, bool FP8>
 cudaError_t attn_launch_one(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(l.grid), 1, 1);
-    cfg.blockDim = dim3(AttnTune<DT, FP8>::kWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(attn_smem<DT, NB, FP8>());
+    cfg.blockDim = dim3(AttnShape<DT, NB, FP8>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(AttnShape<DT, NB, FP8>::kSmem);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(
-        &cfg, attn_decode_kernel<DT, NB, FP8, AttnTune<DT, FP8>::kWarps, AttnTune<DT, FP8>::kStages>, p);
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DT, NB, FP8>, p);
 }
 
 // The status word of this translation unit.

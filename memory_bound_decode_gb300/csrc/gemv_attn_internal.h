@@ -16,7 +16,6 @@ bool api_pdl_enabled();
 
 // ---- attention ----------------------------------------------------------------
 
-constexpr int kAttnSlice = 16;            // tokens a warp takes at a time (one MMA tile)
 constexpr int kAttnTickets = 1024;        // join counters at the start of the workspace
 constexpr int kAttnMaxGroup = 1024;       // query heads per key-value head
 
@@ -39,6 +38,8 @@ struct AttnParams {
     int64_t rows;               // rows of q and out
     int32_t requests, q_heads, kv_heads, group, qtiles;
     int32_t head_dim, page_size, table_width, num_pages, window, max_len;
+    int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
+    int32_t min_slices;         // slices a CTA takes at least
     float scale, softcap;
 };
 
@@ -46,7 +47,7 @@ struct AttnLaunch {
     int dt;            // head size the instance is built for: 64, 128 or 256
     int nb;            // blocks of 8 query heads a CTA carries
     int fp8;
-    int warps, stages, smem_bytes;
+    int warps;
     int qtiles, grid;
     int64_t workspace_bytes;
 };
