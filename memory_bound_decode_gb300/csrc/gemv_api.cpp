@@ -623,6 +623,23 @@ namespace gemv {
 int api_device_state(int* sm_count) { return device_state(sm_count); }
 int api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
 bool api_pdl_enabled() { return pdl_enabled(); }
+bool api_on_current_device(const void* p) { return on_current_device(p); }
+
+bool api_encode_pool(CUtensorMap* map, const void* base, bool fp8, const int64_t (&dims)[4],
+                     const int64_t (&strides)[3], int cols, int rows) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint32_t elem[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(rows), 1, 1};
+    cuuint64_t d[4], st[3];
+    for (int i = 0; i < 4; ++i) d[i] = static_cast<cuuint64_t>(dims[i]);
+    for (int i = 0; i < 3; ++i) st[i] = static_cast<cuuint64_t>(strides[i]);
+    const int line = cols * (fp8 ? 1 : 2);
+    return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+              d, st, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace gemv
 

@@ -3,7 +3,6 @@
 // the paged decode attention.
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include <cuda_runtime.h>
 
@@ -267,7 +266,9 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     char* ws = static_cast<char*>(a->workspace);
     p.ticket = reinterpret_cast<uint32_t*>(ws);
     p.part = reinterpret_cast<float*>(ws + gemv::kAttnTickets * 4);
-    p.part_ml = p.part + static_cast<int64_t>(l.grid) * 2 * l.nb * 8 * l.dt;
+    const int64_t heads = static_cast<int64_t>(l.grid) * l.nb * 8;
+    p.part_warp = p.part + heads * 2 * l.dt;
+    p.part_ml = p.part_warp + heads * gemv::kAttnWarps * l.dt;
     p.q_stride = a->q_stride;
     p.out_stride = a->out_stride;
     p.table_stride = a->table_stride;
@@ -290,8 +291,21 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     if ((c->page_size & (c->page_size - 1)) == 0)
         for (p.page_shift = 0; (1 << p.page_shift) < c->page_size; ++p.page_shift) {
         }
-    p.min_slices = 8;
-    if (const char* v = std::getenv("GEMV_ATTN_MIN")) p.min_slices = atoi(v);
+    // Tensor copies where a box of at least 8 slots (the swizzle's pattern) divides page and slice.
+    const int64_t es = elem_bytes(c);
+    int rows = 1;
+    while (rows < l.slice && c->page_size % (2 * rows) == 0) rows *= 2;
+    if (rows >= 8 && gemv::api_on_current_device(c->k) && gemv::api_on_current_device(c->v)) {
+        const int64_t dims[4] = {c->head_dim, c->page_size, c->kv_heads, c->num_pages};
+        // The stride of a dimension of one entry is never used, but has to be a legal one.
+        const int64_t st[3] = {c->page_size > 1 ? p.slot_stride : c->head_dim * es,
+                               c->kv_heads > 1 ? p.head_stride : c->head_dim * es,
+                               c->num_pages > 1 ? p.page_stride : c->head_dim * es};
+        const int line = l.dt * es < 128 ? l.dt : static_cast<int>(128 / es);
+        p.tma = gemv::api_encode_pool(&p.kmap, c->k, fp8, dims, st, line, rows) &&
+                gemv::api_encode_pool(&p.vmap, c->v, fp8, dims, st, line, rows);
+        p.box_rows = rows;
+    }
     p.scale = a->scale;
     p.softcap = a->softcap;
     return finish(gemv::launch_attn(p, l, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));

@@ -6,25 +6,38 @@
 
 namespace gemv {
 
-template <int DT, int NB, bool FP8>
-cudaError_t attn_prepare_one() {
-    return cudaFuncSetAttribute(attn_decode_kernel<DT, NB, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                AttnShape<DT, NB, FP8>::kSmem);
+template <int DT, int NB, bool FP8, bool TMA>
+cudaError_t attn_prepare_form() {
+    return cudaFuncSetAttribute(attn_decode_kernel<DT, NB, FP8, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                AttnShape<DT, NB, FP8, TMA>::kSmem);
 }
 
 template <int DT, int NB, bool FP8>
-cudaError_t attn_launch_one(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl) {
+cudaError_t attn_prepare_one() {
+    const cudaError_t e = attn_prepare_form<DT, NB, FP8, true>();
+    return e == cudaSuccess ? attn_prepare_form<DT, NB, FP8, false>() : e;
+}
+
+template <int DT, int NB, bool FP8, bool TMA>
+cudaError_t attn_launch_form(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl) {
+    using S = AttnShape<DT, NB, FP8, TMA>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(l.grid), 1, 1);
-    cfg.blockDim = dim3(AttnShape<DT, NB, FP8>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(AttnShape<DT, NB, FP8>::kSmem);
+    cfg.blockDim = dim3(S::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(S::kSmem);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DT, NB, FP8>, p);
+    return cudaLaunchKernelEx(&cfg, attn_decode_kernel<DT, NB, FP8, TMA>, p);
+}
+
+template <int DT, int NB, bool FP8>
+cudaError_t attn_launch_one(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl) {
+    return p.tma ? attn_launch_form<DT, NB, FP8, true>(p, l, s, pdl)
+                 : attn_launch_form<DT, NB, FP8, false>(p, l, s, pdl);
 }
 
 // The status word of this translation unit.

@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>   // CUtensorMap (the type only)
 #include <cuda_runtime.h>
 
 namespace gemv {
@@ -13,13 +14,32 @@ namespace gemv {
 int api_device_state(int* sm_count);      // set-up of the current device; GEMV_OK or an error
 int api_cuda_fail(cudaError_t e);         // record e for gemv_last_cuda_error; GEMV_ERR_CUDA
 bool api_pdl_enabled();
+bool api_on_current_device(const void* p);   // whether p points into the current device's own memory
+// A pool as a 4-D view (column, slot, head, page; strides in bytes) in boxes of
+// `cols` columns x `rows` slots, swizzled; false if the driver rejects it.
+bool api_encode_pool(CUtensorMap* map, const void* base, bool fp8, const int64_t (&dims)[4],
+                     const int64_t (&strides)[3], int cols, int rows);
 
 // ---- attention ----------------------------------------------------------------
 
 constexpr int kAttnTickets = 1024;        // join counters at the start of the workspace
 constexpr int kAttnMaxGroup = 1024;       // query heads per key-value head
 
+constexpr int kAttnWarps = 8;
+constexpr int kAttnRing = 16384;          // bytes of K and V in flight per warp
+
+// Tokens a warp takes at a time: MMA tiles of 16 side by side hide each other's
+// latency and share one reduction (BF16 at 128 columns: 9.3 TB/s of K and V
+// with 16 tokens, 15.3 with 32, K and V from the L2). 64 with an FP8 cache and
+// one block of heads, whose codes take longest to get through; 16 where the
+// accumulators leave no registers, or the ring no room, for more. Without
+// tensor copies a lane copies a token's rows: 32 at most.
+constexpr int attn_slice(int dt, int nb, bool fp8, bool tma) {
+    return (dt == 256 && (!fp8 || nb == 2)) || nb == 4 ? 16 : fp8 && nb == 1 && dt <= 128 && tma ? 64 : 32;
+}
+
 struct AttnParams {
+    CUtensorMap kmap, vmap;     // views of the pools, if tma
     const uint16_t* q;          // BF16
     uint16_t* out;              // BF16
     float* lse;
@@ -30,8 +50,9 @@ struct AttnParams {
     const unsigned char* vc;
     const float* k_scale;
     const float* v_scale;
-    float* part;                // partial outputs of rows cut between CTAs
-    float* part_ml;             // their maxima and sums
+    float* part;                // two pieces per CTA, of rows cut between CTAs: outputs,
+    float* part_ml;             // maxima and sums
+    float* part_warp;           // a piece per warp, of rows cut between a CTA's warps
     uint32_t* ticket;
     int64_t q_stride, out_stride, table_stride;
     int64_t page_stride, head_stride, slot_stride;   // bytes
@@ -39,7 +60,8 @@ struct AttnParams {
     int32_t requests, q_heads, kv_heads, group, qtiles;
     int32_t head_dim, page_size, table_width, num_pages, window, max_len;
     int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
-    int32_t min_slices;         // slices a CTA takes at least
+    int32_t tma;                // 1: tensor copies of box_rows slots
+    int32_t box_rows;
     float scale, softcap;
 };
 
@@ -48,6 +70,7 @@ struct AttnLaunch {
     int nb;            // blocks of 8 query heads a CTA carries
     int fp8;
     int warps;
+    int slice;         // tokens a warp takes at a time
     int qtiles, grid;
     int64_t workspace_bytes;
 };

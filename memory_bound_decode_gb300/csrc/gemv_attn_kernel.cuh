@@ -6,13 +6,17 @@
 // of a softmax kept in FP32, so K and V are read once and no score is stored.
 //
 // Work split. A row is one (request, key-value head) pair; its tokens are cut
-// into slices of 32 or 16. All slices of all rows form one list (request-major), and
-// each CTA takes an equal, contiguous range of it, whatever the lengths are:
-// the lengths live on the device, so every CTA sums them itself. Inside a CTA
-// the warps take the range's slices in turn. A row inside one range is
-// finished there; a row cut between CTAs leaves FP32 partial results (output,
-// maximum, sum) in the workspace and the CTA that arrives last joins them in
-// list order, so the result does not depend on which one that is.
+// into slices of 32 or 16. All slices of all rows form one list
+// (request-major); each CTA takes an equal, contiguous range of it, and each
+// warp an equal, contiguous part of that, whatever the lengths are: the lengths
+// live on the device, so every CTA sums them itself. A warp works through its
+// part alone, row after row, without a barrier of the CTA: rows of a few
+// hundred tokens cost no more than their bytes. A row inside one warp's part
+// is finished there. Of the others each warp has two pieces at most, its first
+// and its last; the CTA joins its warps' pieces once, at the end, and a row
+// cut between CTAs is joined by the CTA that arrives last, through the
+// workspace. Pieces (FP32 output, maximum, sum) are always joined in list
+// order, so the result does not depend on which CTA that is.
 //
 // Tiles. The group of query heads that share a key-value head are the narrow
 // side (N = 8) of the MMAs, 16 tokens of a slice (scores) or 16 columns of
@@ -24,29 +28,58 @@
 #pragma once
 
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "gemv_attn_internal.h"
+#include "gemv_common.cuh"
 
 namespace gemv {
 
 static __device__ unsigned int g_attn_status;
-constexpr unsigned int kStatusBadPage = 2u;
+constexpr unsigned int kStatusBadPage = 2u;   // kStatusWaitTimeout (1) too
 
 namespace attn {
 
-__device__ __forceinline__ uint32_t sm_addr(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+// This thread's arrival at the barrier, once its copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
+}
+// One box of the pool's 4-D view (column, slot, head, page).
+__device__ __forceinline__ void copy_box(uint32_t dst, const void* map, int col, int slot, int head, int page,
+                                         uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 :: "r"(dst), "l"(map), "r"(col), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
+}
+// Wait for the barrier's phase, for at most kMbarWaitLimit rounds; false (and the status bit) if they ran out.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < kMbarWaitLimit; ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred P1;\n\tmbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
+                     "selp.b32 %0, 1, 0, P1;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+    }
+    atomicOr(&g_attn_status, kStatusWaitTimeout);
+    return false;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -76,10 +109,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 codes (low 16 bits of v) to two FP16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t v) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
+// Four E4M3 codes to FP16, exactly: the low two to lo, the high two to hi.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(v));
+}
+// 2^x; below 2^-126: 0.
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
@@ -101,7 +139,7 @@ __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(
 // Tokens of request r that its query can reach: its length, cut to what its
 // row of the table holds (with a status bit); 0 for an empty request, negative
 // for one that has no query row in this call.
-__device__ __forceinline__ int attn_len(const AttnParams& p, int r) {
+static __device__ __noinline__ int attn_len(const AttnParams& p, int r) {
     int len = p.lens[r];
     if (p.token_start) {
         const int a = p.token_start[r], b = p.token_start[r + 1];
@@ -117,6 +155,8 @@ __device__ __forceinline__ int attn_len(const AttnParams& p, int r) {
     }
     return len;
 }
+// a / b, out of line: lists of 2^31 slices are legal, not usual.
+static __device__ __noinline__ int64_t attn_div(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t attn_row(const AttnParams& p, int r) {
     return p.token_start ? static_cast<int64_t>(p.token_start[r + 1]) - 1 : r;
 }
@@ -128,63 +168,89 @@ __device__ __forceinline__ int attn_slices(const AttnParams& p, int len) {
     return len <= 0 ? 0 : (len + TS - 1) / TS - attn_begin(p, len) / TS;
 }
 
-// The slice of an instance: 32 tokens (two MMA tiles side by side hide each
-// other's latency and share one reduction), 16 where two would not fit the
-// registers or the ring.
-template <int DT, int NB, bool FP8>
+// DT: head size of the instance (head_dim <= DT; columns past head_dim are
+// zero). NB: blocks of 8 query heads.
+template <int DT, int NB, bool FP8, bool TMA>
 struct AttnShape {
-    static constexpr int kWarps = 8;
+    static constexpr int kWarps = kAttnWarps;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kSlice = (DT == 256 && !FP8) || (DT == 256 && NB == 2) || NB == 4 ? 16 : 32;
+    static constexpr int kSlice = attn_slice(DT, NB, FP8, TMA);
     static constexpr int kRowBytes = DT * (FP8 ? 1 : 2);
     static constexpr int kEntry = kSlice * kRowBytes;                // K or V of one slice
-    static constexpr int kEntries = 196608 / (kWarps * kEntry) < 12 ? 196608 / (kWarps * kEntry) : 12;
-    static constexpr int kRing = kWarps * kEntries * kEntry;
-    // The warps' results meet in shared memory 8 heads and at most 128 columns at a time; behind the columns of
-    // a head stand its maximum and sum.
-    static constexpr int kPartCols = DT < 128 ? DT : 128;
-    static constexpr int kPartStride = kPartCols + 4;
-    static constexpr int kPart = kWarps * 8 * kPartStride * 4;
-    // Query fragments stay in registers, or (in the same memory as kPart: they are not needed together) in shared
-    // memory where the accumulators leave no registers for them.
+    static constexpr int kEntries = kAttnRing / kEntry < 8 ? kAttnRing / kEntry : 8;
+    static constexpr int kRing = kWarps * kAttnRing;
+    static_assert(kEntry % 1024 == 0, "entries start where the swizzle's pattern does");
+    // A warp's last piece takes the place of its ring when that is empty.
+    static_assert(NB * 8 * DT * 4 <= kAttnRing, "a piece fits the ring");
+    // Query fragments stay in registers where the accumulators leave room for them; else the products read them
+    // from shared memory each time. Either way a warp keeps the queries of a row there as they come, heads apart in
+    // banks (32-bit reads of BF16, 64-bit ones of FP16).
     static constexpr bool kQueryShared = NB == 4 || (DT == 256 && NB == 2);
-    static constexpr int kSmem = kRing + kPart;
-    static_assert(!kQueryShared || (DT / 16) * NB * 256 <= kPart, "query fragments fit");
+    static constexpr int kRawStride = DT * 2 + (FP8 ? 32 : 16);
+    static constexpr int kRaw = NB * 8 * kRawStride;
+    // A warp's first piece waits in shared memory for the others where there is room, else in the workspace.
+    static constexpr int kFirst = NB * 8 * DT * 4;
+    static constexpr bool kFirstShared = kRing + kWarps * (kRaw + kFirst) + 8192 <= 232448;
+    static constexpr int kSmem = kRing + kWarps * (kRaw + (kFirstShared ? kFirst : 0));
+    static_assert(kSmem + 8192 <= 232448, "shared memory");
 };
 
-template <int DT, int NB, bool FP8>
-__global__ void __launch_bounds__(AttnShape<DT, NB, FP8>::kThreads, 1)
+template <int DT, int NB, bool FP8, bool TMA>
+__global__ void __launch_bounds__(AttnShape<DT, NB, FP8, TMA>::kThreads, 1)
 attn_decode_kernel(const __grid_constant__ AttnParams p) {
-    using S = AttnShape<DT, NB, FP8>;
+    using S = AttnShape<DT, NB, FP8, TMA>;
     using namespace attn;
     constexpr int W = S::kWarps, T = S::kThreads, TS = S::kSlice, MT = TS / 16, E = S::kEntries;
     constexpr int RB = S::kRowBytes;
     constexpr int CPR = RB / 16;          // 16-byte chunks of a row
     constexpr int KS = DT / 16;           // MMA steps along the head
+    constexpr int H = NB * 8;             // query heads of a piece
     constexpr float kNegInf = -INFINITY;
     constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-    extern __shared__ __align__(128) unsigned char smem[];
-    float* const part_s = reinterpret_cast<float*>(smem + S::kRing);
-    uint2* const q_s = reinterpret_cast<uint2*>(smem + S::kRing);
+    // A piece of a row: slices s .. s + seg - 1 of ns, the first of them slice `at` of the CTA's range.
+    struct Piece {
+        int valid, r, h, s, seg, ns, at;
+        float v_scale;
+    };
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint64_t s_bar[W * E];     // one per ring entry: its copies have landed
+    __shared__ uint64_t s_qbar[W];        // the same for a warp's queries
+    __shared__ Piece s_piece[2 * W];      // each warp's first and last
+    __shared__ float2 s_ml[2 * W][H];     // their maxima and sums
     __shared__ int32_t s_len[T];          // lengths of requests len0 .. len0 + T - 1
     __shared__ int64_t s_scan[W];
-    __shared__ int64_t s_off;
-    __shared__ int32_t s_r0;
-    __shared__ int32_t s_last;
+    __shared__ int32_t s_longest[W];
+    __shared__ int64_t s_off[W];
+    __shared__ float s_scales[W][2];      // FP8: scales of k and v of the row that q_raw holds
+    __shared__ int32_t s_req[W];
+    __shared__ int32_t s_last[2];
 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int qt = blockIdx.x % p.qtiles;
     const int cta = blockIdx.x / p.qtiles;
     const int ctas = gridDim.x / p.qtiles;
-    const int head0 = qt * NB * 8;                                  // first query head of the group
-    const int nh = min(NB * 8, p.group - head0);                    // query heads of this tile
+    const int head0 = qt * H;                                        // first query head of the group
+    const int nh = min(H, p.group - head0);                          // query heads of this tile
+    unsigned char* const ring_p = smem + w * kAttnRing;
+    unsigned char* const q_raw = smem + S::kRing + w * S::kRaw;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_launch_dependents();
+    if (lane == 0) {
+        // A tensor copy counts its bytes (one arrival arms the barrier), per-thread copies arrive for each lane.
+        for (int i = 0; i < E; ++i) mbar_init(&s_bar[w * E + i], TMA ? 1 : 32);
+        mbar_init(&s_qbar[w], 32);
+        fence_mbar_init_cluster();
+        s_req[w] = -1;
+        s_scales[w][0] = s_scales[w][1] = 1.f;
+        s_piece[2 * w].valid = s_piece[2 * w + 1].valid = 0;
+    }
+    for (int i = lane; i < S::kRaw / 16; i += 32) reinterpret_cast<uint4*>(q_raw)[i] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    pdl_wait_prerequisites();
 
-    // The sum of the slices, and (in the first chunk of T requests) their running sums.
+    // ---- the sum of the slices, and (in the first chunk of requests) their running sums ----
     const int len_first = tid < p.requests ? attn_len(p, tid) : -1;
     const int n_first = attn_slices<TS>(p, len_first);
     s_len[tid] = len_first;
@@ -194,21 +260,24 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    if (lane == 31) s_scan[w] = incl;
-    if (tid == 0) s_r0 = -1;
+    int longest = __reduce_max_sync(0xffffffffu, n_first);
+    if (lane == 31) {
+        s_scan[w] = incl;
+        s_longest[w] = longest;
+    }
     __syncthreads();
     int64_t carry = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         if (i < w) incl += s_scan[i];
         carry += s_scan[i];
+        longest = max(longest, s_longest[i]);
     }
     int64_t total = carry;
     if (p.requests > T) {
         int64_t more = 0;
-        for (int r = T + tid; r < p.requests; r += T) {
-            more += attn_slices<TS>(p, attn_len(p, r));
-        }
+#pragma unroll 1
+        for (int r = T + tid; r < p.requests; r += T) more += attn_slices<TS>(p, attn_len(p, r));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
         __syncthreads();
@@ -228,22 +297,31 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             for (int i = tid; i < p.q_heads; i += T) p.lse[row * p.q_heads + i] = kNegInf;
     }
 
-    // This CTA's range, f0 .. f0 + cnt, of the list of slices, and the request that f0 falls in.
+    // ---- the CTA's range f0 .. f0 + cnt of the list, this warp's part of it, and the requests the parts begin in ----
     total *= p.kv_heads;
-    const int64_t quota = max((total + ctas - 1) / ctas, static_cast<int64_t>(p.min_slices));
+    // At least a slice per warp; and rows of up to four per warp are better not cut between CTAs: the last of four
+    // slices comes 2 us after the first, a join across CTAs takes 4.
+    const int least = max(W, longest <= 4 * W ? longest : 0);
+    const int64_t quota = max(total >> 31 ? attn_div(total + ctas - 1, ctas)
+                                          : static_cast<int64_t>((static_cast<uint32_t>(total) + ctas - 1) / ctas),
+                              static_cast<int64_t>(least));
     const int64_t f0 = cta * quota;
     if (f0 >= total) return;
     const int cnt = static_cast<int>(min(quota, total - f0));
+    const int part = (cnt + W - 1) / W;
     auto claim = [&](int r, int n, int64_t end) {                    // `end`: slices up to request r, a head
-        const int64_t lo = (end - n) * p.kv_heads;
-        if (lo <= f0 && f0 < end * p.kv_heads) {
-            s_r0 = r;
-            s_off = f0 - lo;
-        }
+        const int64_t lo = (end - n) * p.kv_heads - f0, hi = end * p.kv_heads - f0;
+#pragma unroll 1
+        for (int i = 0; i < W && n > 0; ++i)
+            if (lo <= i * part && i * part < hi) {
+                s_req[i] = r;
+                s_off[i] = i * part - lo;
+            }
     };
     claim(tid, n_first, incl);
     int len0 = 0;
-    for (int base = T; base < p.requests && carry * p.kv_heads <= f0; base += T) {   // the same for all threads
+#pragma unroll 1
+    for (int base = T; base < p.requests && carry * p.kv_heads < f0 + cnt; base += T) {   // the same for all threads
         const int len = base + tid < p.requests ? attn_len(p, base + tid) : -1;
         const int n = attn_slices<TS>(p, len);
         incl = n;
@@ -252,7 +330,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        __syncthreads();                                            // s_scan and s_len have been read
+        __syncthreads();                                             // s_scan and s_len have been read
         if (lane == 31) s_scan[w] = incl;
         s_len[tid] = len;
         len0 = base;
@@ -266,124 +344,229 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         claim(base + tid, n, before + incl);
     }
     __syncthreads();
-    const int r0 = s_r0;
-    if (r0 < 0) return;                                             // only if lens changed under the call
-    auto len_of = [&](int r) { return r - len0 < T ? s_len[r - len0] : attn_len(p, r); };
+    auto len_of = [&](int r) { return r >= len0 && r - len0 < T ? s_len[r - len0] : attn_len(p, r); };
+    int left = max(0, min(part, cnt - w * part));                    // slices of this warp
+    int r = s_req[w];
+    if (r < 0) left = 0;                                             // no part (or lens changed under the call)
+    int h = 0, s = 0;
+    if (left > 0) {
+        const int ns0 = max(1, attn_slices<TS>(p, len_of(r)));
+        h = s_off[w] >> 31 ? static_cast<int>(attn_div(s_off[w], ns0)) : static_cast<int>(s_off[w]) / ns0;
+        s = static_cast<int>(s_off[w] - static_cast<int64_t>(h) * ns0);
+    }
 
-    const int ns0 = max(1, attn_slices<TS>(p, len_of(r0)));
-    const int h_first = s_off >> 31 ? static_cast<int>(s_off / ns0) : static_cast<int>(s_off) / ns0;
-    const int s_first = static_cast<int>(s_off - static_cast<int64_t>(h_first) * ns0);
+    // ---- queries of a row, as they come, into q_raw ----
+    auto fetch_query = [&](int64_t row, int hk) {
+        const unsigned char* src = reinterpret_cast<const unsigned char*>(
+            p.q + row * p.q_stride + (static_cast<int64_t>(hk) * p.group + head0) * p.head_dim);
+        const int per = p.head_dim / 4;                              // 8-byte pieces of a head
+        const uint32_t to = smem_addr(q_raw);
+#pragma unroll 1
+        for (int hd = 0; hd < nh; ++hd)
+#pragma unroll 1
+            for (int i = lane; i < per; i += 32) copy8(to + hd * S::kRawStride + i * 8, src + (hd * per + i) * 8);
+        if (FP8 && lane < 2 && (lane ? p.v_scale : p.k_scale))
+            copy4(smem_addr(&s_scales[w][lane]), (lane ? p.v_scale : p.k_scale) + hk);
+        copies_arrive(smem_addr(&s_qbar[w]));
+    };
 
     // ---- copies of K and V into this warp's ring: entries K0 V0 K1 V1 ..., E of them at a time ----
-    const uint32_t ring = sm_addr(smem) + static_cast<uint32_t>(w) * E * S::kEntry;
-    const int warp_slices = cnt > w ? (cnt - w + W - 1) / W : 0;
+    //
+    // An entry holds the rows of a slice as lines of 128 bytes (one, two or four per row, each line's rows together)
+    // with 16-byte chunk c of row r at c ^ (r & 7), the tensor copies' 128-byte swizzle; rows of 64 bytes with the
+    // 64-byte one. Tensor copies move boxes of box_rows slots of one page (box_rows divides page and slice), a
+    // lane per box and line. Where pages are no multiple of 8 slots, or lie outside this GPU's memory, every thread
+    // copies 16-byte chunks.
+    using Mask = std::conditional_t<TS == 64, uint64_t, uint32_t>;   // tokens of a slice
+    constexpr Mask kAll = static_cast<Mask>(~0ull >> (64 - TS));
+    constexpr int LINES = RB < 128 ? 1 : RB / 128, LB = RB < 128 ? RB : 128;
+    const uint32_t ring = smem_addr(ring_p);
+    const uint32_t bars = smem_addr(s_bar) + static_cast<uint32_t>(w) * E * 8;
+    const int mine = left;                // slices of this warp
     const int chunks = p.head_dim * (FP8 ? 1 : 2) / 16;
-    int pr = r0, ph = h_first, ps = s_first, pns = ns0, plen = len_of(r0);
-    int issued = 0;                       // entries
-    uint32_t valid_of = 0;                // lane i: the visible tokens of slice i (modulo 32)
-    int next_page = -1, next_in = -1;     // lane i: page and place of token i of the next slice
-    int next_h = 0;
-    int64_t off = -1;                     // lane i: byte offset of token i of the slice whose K went out last
-    auto settle = [&](int step) {         // move the cursor on by `step` slices and look up the pages there
-        ps += step;
-        while (ps >= pns) {
-            ps -= pns;
-            if (++ph == p.kv_heads) {
-                ph = 0;
-                do {
-                    if (++pr >= p.requests) {                        // only if lens changed under the call
-                        plen = 0;
-                        pns = 0x7fffffff;
-                        break;
-                    }
-                    plen = len_of(pr);
-                    pns = attn_slices<TS>(p, plen);
-                } while (pns == 0);
-            }
-        }
-        const int begin = attn_begin(p, plen);
-        const int tok = (begin / TS + ps) * TS + (lane & (TS - 1));
-        const bool in = tok >= begin && tok < plen;
-        const int blk = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
-        next_in = in ? tok - blk * p.page_size : -1;
-        next_page = in ? p.table[pr * p.table_stride + blk] : -1;
-        next_h = ph;
+    int issued = 0, slot_at = 0;          // slices (their K), and the next entry's place in the ring
+    Mask valid_of = 0;                    // lane i: the visible tokens of slice i (modulo 32)
+    int64_t off = 0;                      // of the slice whose K went out last, lane i: byte offset of token i;
+    int box_page = 0, box_in = 0, box_h = 0;   // page, place in it and head of box i
+    Mask last_valid = 0;                  // and its visible tokens
+
+    // Pages are looked up for a batch of slices at a time, a lane per box (per token without tensor copies), and
+    // a batch ahead: a look-up takes as long as all the copies in flight before it (3 us under load).
+    const int box = TMA ? p.box_rows : 1;
+    const int per_slice = TS / box, batch = 32 / per_slice;          // lanes a slice, slices a batch
+    struct Look {
+        int r, h, s;                      // the slice
+        int page, in;                     // in: the box's first slot in the page, -1 if no token of it is visible
+        Mask valid;                       // the slice's visible tokens
     };
-    auto copy_rows = [&](const unsigned char* base, uint32_t dst0) {
-#pragma unroll
-        for (int i = 0; i < TS * CPR / 32; ++i) {
-            const int idx = i * 32 + lane, row = idx / CPR, ch = idx % CPR;
-            const int64_t o = __shfl_sync(0xffffffffu, off, row);
-            const int sw = CPR >= 8 ? row & 7 : (row >> 1) & 3;
-            const int n = o >= 0 && ch < chunks ? 16 : 0;            // 0: the chunk is filled with zeros
-            copy16(dst0 + row * RB + ((ch ^ sw) << 4), base + (n ? o + ch * 16 : 0), n);
-        }
-    };
-    auto issue = [&]() {
-        const int slice = issued >> 1;
-        if (slice < warp_slices) {
-            const uint32_t dst = ring + (issued % E) * S::kEntry;
-            if ((issued & 1) == 0) {
-                off = -1;
-                if (next_in >= 0) {
-                    if (next_page >= 0 && next_page < p.num_pages)
-                        off = next_page * p.page_stride + next_h * p.head_stride + next_in * p.slot_stride;
-                    else
-                        atomicOr(&g_attn_status, kStatusBadPage);
-                }
-                const uint32_t valid = __ballot_sync(0xffffffffu, off >= 0);
-                if (lane == (slice & 31)) valid_of = valid;
-                copy_rows(p.kc, dst);
-                if (slice + 1 < warp_slices) settle(W);
-            } else {
-                copy_rows(p.vc, dst);
-            }
-        }
-        ++issued;
-        copy_commit();
-    };
-    if (warp_slices > 0) settle(w);
+    Look now = {}, then = {};
+    then.r = r;
+    then.h = h;
+    then.s = s - 1;                       // the slice before the first
+    int looked = 0;                       // slices up to the end of `then`; `now` is the batch before it
+    auto look_ahead = [&]() {             // `then` becomes the batch after it
+        now = then;
+        const int last = looked ? (batch - 1) * per_slice : 0;       // a lane of its last slice
+        const int idx = lane / per_slice;
+        int ur = __shfl_sync(0xffffffffu, then.r, last), uh = __shfl_sync(0xffffffffu, then.h, last);
+        int us = __shfl_sync(0xffffffffu, then.s, last) + 1 + idx;
+        then.page = then.in = -1;
+        if (looked + idx < mine) {
+            int len = len_of(ur), ns = max(1, attn_slices<TS>(p, len));
 #pragma unroll 1
-    for (int i = 0; i < E; ++i) issue();
-
-    // ---- rows of the range, one after the other ----
-    int r = r0, h = h_first, s = s_first, done = 0, li = w, taken = 0;   // taken: entries
-    while (done < cnt) {
-        const int len = len_of(r);
-        const int ns = attn_slices<TS>(p, len);
-        const int seg = min(ns - s, cnt - done);
-        if (seg <= 0) break;
-        const int64_t row = attn_row(p, r);
-        const int64_t head_at = static_cast<int64_t>(h) * p.group + head0;
-
-        // Query fragments (B operand: 16 columns of the head x 8 heads).
-        uint32_t qf[S::kQueryShared ? 1 : KS][S::kQueryShared ? 1 : NB][2];
-        float col_scale[NB][2];
-        auto load_query = [&](int nb, int ks, uint32_t (&f)[2]) {
-            const bool in = nb * 8 + g < nh;
-            const uint16_t* qp = p.q + row * p.q_stride + (head_at + nb * 8 + g) * p.head_dim;
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int d = ks * 16 + b * 8 + 2 * t;
-                    f[b] = in && d < p.head_dim ? *reinterpret_cast<const uint32_t*>(qp + d) : 0u;
+            while (us >= ns) {
+                us -= ns;
+                if (++uh == p.kv_heads) {
+                    uh = 0;
+#pragma unroll 1
+                    do {
+                        if (++ur >= p.requests) {                    // only if lens changed under the call
+                            len = 0;
+                            ns = 0x7fffffff;
+                            break;
+                        }
+                        len = len_of(ur);
+                        ns = attn_slices<TS>(p, len);
+                    } while (ns == 0);
                 }
-            } else {
-                const int d = ks * 16 + 4 * t;
-                const uint2 v = in && d < p.head_dim ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
-                f[0] = v.x;
-                f[1] = v.y;
             }
-        };
-        if constexpr (S::kQueryShared) __syncthreads();              // part_s has been read
+            const int begin = attn_begin(p, len);
+            const int first = (begin / TS + us) * TS;
+            const int lo = max(begin - first, 0), hi = min(len - first, TS);
+            then.valid = kAll >> (TS - max(hi, 1)) & kAll << lo;     // lo < TS; hi >= 1 in a row of the list
+            then.r = ur;
+            then.h = uh;
+            then.s = us;
+            const int tok = first + lane % per_slice * box;
+            if (tok < len && tok + box > begin) {
+                const int blk = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
+                then.in = tok - blk * p.page_size;
+                then.page = p.table[ur * p.table_stride + blk];
+            }
+        }
+        looked += batch;
+    };
+    constexpr int LPR = CPR < 8 ? CPR : 8, RPI = 32 / LPR;
+    const int crow = lane / LPR, cch = lane % LPR;
+    auto copy_rows = [&](const unsigned char* base, uint32_t dst0) {
+        const unsigned char* const at = base + cch * 16;
+        const bool full = last_valid == kAll && chunks == CPR;
+#pragma unroll
+        for (int i = 0; i < TS / RPI; ++i) {
+            const int row = i * RPI + crow;
+            const unsigned char* const src = at + __shfl_sync(0xffffffffu, off, row);
+            const int sw = CPR >= 8 ? row & 7 : (row >> 1) & 3;
+            const uint32_t dst = dst0 + row * LB + ((cch ^ sw) << 4);
+#pragma unroll
+            for (int c = 0; c < LINES; ++c) {
+                if (full) {
+                    copy16(dst + c * TS * 128, src + c * 128);
+                } else {
+                    const bool in = (last_valid >> row & 1u) && c * LPR + cch < chunks;   // else zeros
+                    copy16_or_zero(dst + c * TS * 128, in ? src + c * 128 : base, in);
+                }
+            }
+        }
+    };
+    auto issue = [&](auto k_or_v) {
+        constexpr bool kIsK = decltype(k_or_v)::value;
+        if (issued < mine) {
+            const uint32_t dst = ring + slot_at * S::kEntry, bar = bars + slot_at * 8;
+            if constexpr (kIsK) {
+#pragma unroll 1
+                while (issued >= looked - batch) look_ahead();
+                const int of = (issued & (batch - 1)) * per_slice, i = TMA ? lane / LINES : lane & (TS - 1);
+                const int page = __shfl_sync(0xffffffffu, now.page, (of + i) & 31);
+                const int place = __shfl_sync(0xffffffffu, now.in, (of + i) & 31);
+                const int head = __shfl_sync(0xffffffffu, now.h, of);
+                last_valid = __shfl_sync(0xffffffffu, now.valid, of);
+                const bool has = i < per_slice && place >= 0;
+                const bool in = has && page >= 0 && page < p.num_pages;
+                const uint32_t bad = __ballot_sync(0xffffffffu, has && !in);
+                if (bad) {                                           // their tokens count as masked
+                    if (lane == 0) atomicOr(&g_attn_status, kStatusBadPage);
+                    const int lines = TMA ? LINES : 1;
+#pragma unroll 1
+                    for (int k = 0; k < TS; ++k)
+                        if (bad >> (k / box * lines) & 1u) last_valid &= ~(Mask(1) << k);
+                }
+                if (lane == (issued & 31)) valid_of = last_valid;
+                if constexpr (TMA) {
+                    box_page = in ? page : p.num_pages;              // outside the view: zeros
+                    box_in = in ? place : 0;
+                    box_h = head;
+                } else {
+                    off = in ? page * p.page_stride + head * p.head_stride + place * p.slot_stride : 0;
+                }
+            }
+            if constexpr (TMA) {
+                if (lane == 0) expect_bytes(bar, S::kEntry);
+                __syncwarp();
+                if (lane < per_slice * LINES)
+                    copy_box(dst + lane % LINES * TS * 128 + lane / LINES * box * LB, kIsK ? &p.kmap : &p.vmap,
+                             lane % LINES * (FP8 ? 128 : 64), box_in, box_h, box_page, bar);
+            } else {
+                copy_rows(kIsK ? p.kc : p.vc, dst);
+                copies_arrive(bar);
+            }
+        }
+        if constexpr (!kIsK) ++issued;
+        slot_at = slot_at + 1 == E ? 0 : slot_at + 1;
+    };
+    using K = std::true_type;
+    using V = std::false_type;
+    if (mine > 0) fetch_query(attn_row(p, r), h);
+#pragma unroll 1
+    for (int i = 0; i < E; ++i) {
+        if (i & 1) issue(V{});
+        else issue(K{});
+    }
+    int taken = 0, take_at = 0;           // slices; the next entry's place in the ring, and its barrier's phase
+    uint32_t phase = 0;
+    bool ok = true;
+    auto landed = [&](bool before) {      // the next entry, for all lanes alike
+        return __all_sync(0xffffffffu, before && wait_phase(bars + take_at * 8, phase)) != 0;
+    };
+    auto next_entry = [&]() {
+        if (++take_at == E) {
+            take_at = 0;
+            phase ^= 1u;
+        }
+    };
+
+    // ---- query fragments (B operand: 16 columns of the head x 8 heads) as the products take them ----
+    constexpr int QN = S::kQueryShared ? 1 : NB;
+    uint32_t qf[QN][KS][2];
+    float col_scale[NB][2];
+    uint32_t q_phase = 0;
+    // Scores leave the first product as powers of two, or (capped) as the argument of tanh.
+    const float score_scale = p.softcap > 0.f ? p.scale / p.softcap : p.scale * kLog2e;
+    const float cap_log2 = p.softcap * kLog2e;
+    auto raw_query = [&](int ks, int nb) {
+        const unsigned char* at = q_raw + (nb * 8 + g) * S::kRawStride + ks * 32;
+        if constexpr (FP8) return *reinterpret_cast<const uint2*>(at + 8 * t);
+        else return make_uint2(*reinterpret_cast<const uint32_t*>(at + 4 * t),
+                               *reinterpret_cast<const uint32_t*>(at + 16 + 4 * t));
+    };
+    float v_scale = 1.f;
+    auto place_query = [&]() {
+        wait_phase(smem_addr(&s_qbar[w]), q_phase);                  // plain loads of this warp: they do land
+        q_phase ^= 1u;
+        const float ksc = score_scale * (FP8 ? s_scales[w][0] : 1.f);
+        v_scale = FP8 ? s_scales[w][1] : 1.f;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+            col_scale[nb][0] = col_scale[nb][1] = ksc;
             uint32_t f[KS][2];
+            if constexpr (!S::kQueryShared || FP8) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) load_query(nb, ks, f[ks]);
-            if constexpr (!FP8) {
-                col_scale[nb][0] = col_scale[nb][1] = p.scale;
-            } else {
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint2 v = raw_query(ks, nb);
+                    f[ks][0] = v.x;
+                    f[ks][1] = v.y;
+                }
+            }
+            if constexpr (FP8) {
                 // The FP8 cache is widened to FP16 (exact); q is brought to FP16 by a power of two per head
                 // that puts its largest value in [1, 2): what that loses is below 2^-24 of that value.
                 float top = 0.f;
@@ -403,27 +586,55 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     for (int b = 0; b < 2; ++b)
                         f[ks][b] = pack_f16(low_bf16(f[ks][b]) * down, high_bf16(f[ks][b]) * down);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                const float ksc = p.scale * (p.k_scale ? p.k_scale[h] : 1.f);
-                col_scale[nb][0] = __shfl_sync(0xffffffffu, up, 8 * t) * ksc;
-                col_scale[nb][1] = __shfl_sync(0xffffffffu, up, 8 * t + 4) * ksc;
-            }
-            if constexpr (S::kQueryShared) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    if (ks % W == w) q_s[(nb * KS + ks) * 32 + lane] = make_uint2(f[ks][0], f[ks][1]);
-            } else {
+                for (int j = 0; j < 2; ++j) col_scale[nb][j] *= __shfl_sync(0xffffffffu, up, 8 * t + 4 * j);
+                if constexpr (S::kQueryShared) {                     // in place: each lane what it read
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+                        *reinterpret_cast<uint2*>(q_raw + (nb * 8 + g) * S::kRawStride + ks * 32 + 8 * t) =
+                            make_uint2(f[ks][0], f[ks][1]);
+                }
+            }
+            if constexpr (!S::kQueryShared) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    qf[ks][nb][0] = f[ks][0];
-                    qf[ks][nb][1] = f[ks][1];
+                    qf[nb][ks][0] = f[ks][0];
+                    qf[nb][ks][1] = f[ks][1];
                 }
             }
         }
-        if constexpr (S::kQueryShared) __syncthreads();
-        auto query = [&](int ks, int nb) {
-            if constexpr (S::kQueryShared) return q_s[(nb * KS + ks) * 32 + lane];
-            else return make_uint2(qf[ks][nb][0], qf[ks][nb][1]);
-        };
+        __syncwarp();                                                // q_raw has been read
+    };
+    auto query = [&](int ks, int nb) {
+        if constexpr (S::kQueryShared) return raw_query(ks, nb);
+        else return make_uint2(qf[nb][ks][0], qf[nb][ks][1]);
+    };
+
+    auto first_piece = [&](int warp) {
+        if constexpr (S::kFirstShared) return reinterpret_cast<float*>(smem + S::kRing + W * S::kRaw + warp * S::kFirst);
+        else return p.part_warp + (static_cast<int64_t>(blockIdx.x) * W + warp) * H * DT;
+    };
+
+    // ---- the rows of this warp's part, one after the other ----
+    int at = w * part;
+    while (left > 0) {
+        const int len = len_of(r);
+        const int ns = attn_slices<TS>(p, len);
+        const int seg = min(ns - s, left);
+        if (seg <= 0) break;                                         // only if lens changed under the call
+        const int64_t row = attn_row(p, r);
+        place_query();
+
+        // The row after this one.
+        int next_r = r, next_h = h;
+        if (seg < left && ++next_h == p.kv_heads) {
+            next_h = 0;
+#pragma unroll 1
+            do ++next_r;
+            while (next_r < p.requests && attn_slices<TS>(p, len_of(next_r)) == 0);
+        }
+        const bool more = seg < left && next_r < p.requests;
+        if (!S::kQueryShared && more) fetch_query(attn_row(p, next_r), next_h);
 
         float m[NB][2], l[NB][2], acc[KS][NB][4];
 #pragma unroll
@@ -436,10 +647,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 for (int j = 0; j < 4; ++j) acc[ks][nb][j] = 0.f;
         }
 
-        for (; li < done + seg; li += W) {
-            copy_wait<E - 1>();
-            __syncwarp();
-            const uint32_t valid = __shfl_sync(0xffffffffu, valid_of, (taken >> 1) & 31);
+#pragma unroll 1
+        for (int step = 0; step < seg; ++step) {
+            if (!(ok = landed(ok))) break;
+            const Mask valid = __shfl_sync(0xffffffffu, valid_of, taken & 31);
 
             // S^T = K Q^T: rows g and g + 8 of a tile are tokens, columns 2t and 2t + 1 heads.
             float sc[MT][NB][4];
@@ -448,7 +659,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) sc[mt][nb][0] = sc[mt][nb][1] = sc[mt][nb][2] = sc[mt][nb][3] = 0.f;
             {
-                const uint32_t kb = ring + (taken % E) * S::kEntry;
+                const uint32_t kb = ring + take_at * S::kEntry;
                 const int arow = lane & 15;
                 const int asw = CPR >= 8 ? arow & 7 : (arow >> 1) & 3;
 #pragma unroll
@@ -456,7 +667,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     uint32_t a[MT][4];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        ldsm4(a[mt], kb + (mt * 16 + arow) * RB + (((c + (lane >> 4)) ^ asw) << 4));
+                        ldsm4(a[mt], kb + c / 8 * TS * 128 + (mt * 16 + arow) * LB +
+                                         (((c % 8 + (lane >> 4)) ^ asw) << 4));
                     if constexpr (!FP8) {
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
@@ -473,10 +685,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                             uint32_t f[MT][4];
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
-                                f[mt][0] = e4m3_pair(a[mt][2 * x]);
-                                f[mt][1] = e4m3_pair(a[mt][2 * x + 1]);
-                                f[mt][2] = e4m3_pair(a[mt][2 * x] >> 16);
-                                f[mt][3] = e4m3_pair(a[mt][2 * x + 1] >> 16);
+                                e4m3_to_f16(a[mt][2 * x], f[mt][0], f[mt][2]);
+                                e4m3_to_f16(a[mt][2 * x + 1], f[mt][1], f[mt][3]);
                             }
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb) {
@@ -490,8 +700,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 }
             }
             __syncwarp();
-            ++taken;
-            issue();                                                 // into the entry just read
+            next_entry();
+            issue(std::bool_constant<E % 2 == 0>{});                 // into the entry just read: E entries on
 
             // Running maximum and sum, in powers of two.
             uint32_t pb[MT][NB][2], pl[FP8 ? 1 : MT][FP8 ? 1 : NB][2];
@@ -501,23 +711,32 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float v = sc[mt][nb][j] * col_scale[nb][j & 1];
-                        if (p.softcap > 0.f) v = p.softcap * tanhf(v / p.softcap);
-                        v *= kLog2e;
-                        x[mt][j] = valid >> (mt * 16 + g + (j & 2) * 4) & 1u ? v : kNegInf;
-                    }
+                    for (int j = 0; j < 4; ++j) x[mt][j] = sc[mt][nb][j] * col_scale[nb][j & 1];
+                if (p.softcap > 0.f) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[mt][j] = cap_log2 * tanhf(x[mt][j]);
+                }
+                if (valid != kAll) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (!(valid >> (mt * 16 + g + (j & 2) * 4) & 1u)) x[mt][j] = kNegInf;
+                }
                 float corr[2], base[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float top = fmaxf(x[0][j], x[0][j + 2]);
-                    if constexpr (MT == 2) top = fmaxf(top, fmaxf(x[1][j], x[1][j + 2]));
+                    #pragma unroll
+                    for (int mt = 1; mt < MT; ++mt) top = fmaxf(top, fmaxf(x[mt][j], x[mt][j + 2]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     top = fmaxf(top, m[nb][j]);
                     base[j] = top == kNegInf ? 0.f : top;
-                    corr[j] = exp2f(m[nb][j] - base[j]);
+                    corr[j] = exp2_ftz(m[nb][j] - base[j]);
                     m[nb][j] = top;
                 }
                 l[nb][0] *= corr[0];
@@ -534,7 +753,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[mt][j] = exp2f(x[mt][j] - base[j & 1]);
+                    for (int j = 0; j < 4; ++j) x[mt][j] = exp2_ftz(x[mt][j] - base[j & 1]);
                     l[nb][0] += x[mt][0] + x[mt][2];
                     l[nb][1] += x[mt][1] + x[mt][3];
                     // P as the B operand. FP16 beside an FP8 cache (2^-12 relative). Beside a BF16 cache P has to
@@ -554,9 +773,22 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             }
 
             // O^T += V^T P^T: rows are columns of the head.
-            copy_wait<E - 1>();
-            __syncwarp();
-            const uint32_t vb = ring + (taken % E) * S::kEntry;
+            if (!(ok = landed(ok))) break;
+            const uint32_t vb = ring + take_at * S::kEntry;
+            if (TMA && valid != kAll) {
+                // A box brings whole rows of the page, also those past the length: 0 * NaN must not get into the sum.
+#pragma unroll 1
+                for (int row = lane; row < TS; row += 32)
+                    if (!(valid >> row & 1u)) {
+#pragma unroll 1
+                        for (int c = 0; c < CPR; ++c) {
+                            const uint32_t to = vb + c / 8 * TS * 128 + row * LB + (c % 8) * 16;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(to), "r"(0) : "memory");
+                        }
+                    }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the entry's next copy
+                __syncwarp();
+            }
             if constexpr (!FP8) {
                 const int vrow = (lane & 7) + ((lane >> 4) << 3);
                 const int vsw = vrow & 7;
@@ -565,7 +797,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         uint32_t a[4];
-                        ldsm4_t(a, vb + (mt * 16 + vrow) * RB + (((2 * ks + ((lane >> 3) & 1)) ^ vsw) << 4));
+                        ldsm4_t(a, vb + ks / 4 * TS * 128 + (mt * 16 + vrow) * LB +
+                                       (((2 * ks % 8 + ((lane >> 3) & 1)) ^ vsw) << 4));
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb) {
                             mma<false>(acc[ks][nb], a[0], a[1], a[2], a[3], pb[mt][nb][0], pb[mt][nb][1]);
@@ -582,13 +815,13 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         uint32_t a[4];
-                        ldsm4_t(a, vb + (mt * 16 + vrow) * RB + (((c + (lane >> 4)) ^ vsw) << 4));
+                        ldsm4_t(a, vb + c / 8 * TS * 128 + (mt * 16 + vrow) * LB +
+                                       (((c % 8 + (lane >> 4)) ^ vsw) << 4));
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
-                            const uint32_t lo = __byte_perm(a[2 * x], 0, 0x3120);
-                            const uint32_t hi = __byte_perm(a[2 * x + 1], 0, 0x3120);
-                            const uint32_t a0 = e4m3_pair(lo), a1 = e4m3_pair(lo >> 16);
-                            const uint32_t a2 = e4m3_pair(hi), a3 = e4m3_pair(hi >> 16);
+                            uint32_t a0, a1, a2, a3;
+                            e4m3_to_f16(__byte_perm(a[2 * x], 0, 0x3120), a0, a1);
+                            e4m3_to_f16(__byte_perm(a[2 * x + 1], 0, 0x3120), a2, a3);
 #pragma unroll
                             for (int nb = 0; nb < NB; ++nb)
                                 mma<true>(acc[c + x][nb], a0, a1, a2, a3, pb[mt][nb][0], pb[mt][nb][1]);
@@ -597,145 +830,243 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             }
             __syncwarp();
             ++taken;
-            issue();
+            next_entry();
+            issue(std::bool_constant<E % 2 == 1>{});
         }
-
-        // ---- the warps' results of this row, joined ----
-        const bool whole = s == 0 && seg == ns;
-        const int64_t piece = static_cast<int64_t>(blockIdx.x) * 2 + (s == 0 ? 1 : 0);
-        const float v_scale = FP8 && p.v_scale ? p.v_scale[h] : 1.f;
-        auto store = [&](int hd, int d, float4 o, float top, float sum) {
-            const float inv = sum == 0.f ? 0.f : v_scale / sum;
-            *reinterpret_cast<uint2*>(p.out + row * p.out_stride + (head_at + hd) * p.head_dim + d) =
-                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-            if (p.lse && d == 0)
-                p.lse[row * p.q_heads + head_at + hd] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
-        };
-        constexpr int KP = S::kPartCols / 16;                        // steps of a round
+        if (!ok) {                                                   // a copy never came: no plausible numbers
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            float sums[2];
+            for (int nb = 0; nb < NB; ++nb) {
+                m[nb][0] = m[nb][1] = 0.f;
+                l[nb][0] = l[nb][1] = __int_as_float(0x7fffffff);
+            }
+        }
+        if (S::kQueryShared && more) fetch_query(attn_row(p, next_r), next_h);
+
+        // ---- what becomes of the row ----
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                sums[j] = l[nb][j];
-                sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], 4);
-                sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], 8);
-                sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], 16);
+                l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 4);
+                l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 8);
+                l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 16);
             }
-            const int heads = min(8, nh - nb * 8);
+        const bool whole = s == 0 && seg == ns, final = seg == left;
+        if (whole) {
+            const int64_t head_at = static_cast<int64_t>(h) * p.group + head0;
 #pragma unroll
-            for (int d0 = 0; d0 < DT; d0 += S::kPartCols) {
-                if (heads <= 0 || d0 >= p.head_dim) continue;
-                __syncthreads();                                     // part_s (or q_s) has been read
-                float* mine_s = part_s + w * 8 * S::kPartStride;
+            for (int nb = 0; nb < NB; ++nb) {
+                float inv[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (2 * t + j < heads) {
-                        float* at = mine_s + (2 * t + j) * S::kPartStride;
-                        if (g == 0) {
-                            at[S::kPartCols] = m[nb][j];
-                            at[S::kPartCols + 1] = sums[j];
-                        }
+                    const int hd = nb * 8 + 2 * t + j;
+                    inv[j] = l[nb][j] == 0.f ? 0.f : v_scale / l[nb][j];
+                    if (p.lse && g == 0 && hd < nh)
+                        p.lse[row * p.q_heads + head_at + hd] =
+                            m[nb][j] == kNegInf ? kNegInf : (m[nb][j] + log2f(l[nb][j])) * kLn2;
+                }
+                // Transposed again, lane (g, t) holds columns 2t, 2t + 1 of the tile's rows for head g.
+                uint16_t* const o = p.out + row * p.out_stride + (head_at + nb * 8 + g) * p.head_dim;
 #pragma unroll
-                        for (int k = 0; k < KP; ++k) {
-                            // row g of the tile: column k * 16 + g (FP8: 2g); row g + 8: + 8 (FP8: + 1)
-                            at[k * 16 + (FP8 ? 2 * g : g)] = acc[d0 / 16 + k][nb][j];
-                            at[k * 16 + (FP8 ? 2 * g + 1 : g + 8)] = acc[d0 / 16 + k][nb][j + 2];
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint32_t a = transpose8x8(pack_bf16(acc[ks][nb][0] * inv[0], acc[ks][nb][1] * inv[1]));
+                    const uint32_t b = transpose8x8(pack_bf16(acc[ks][nb][2] * inv[0], acc[ks][nb][3] * inv[1]));
+                    if (nb * 8 + g < nh && ks * 16 < p.head_dim) {
+                        if constexpr (FP8) {                         // a: even columns, b: odd ones
+                            *reinterpret_cast<uint2*>(o + ks * 16 + 4 * t) =
+                                make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+                        } else {
+                            *reinterpret_cast<uint32_t*>(o + ks * 16 + 2 * t) = a;
+                            if (ks * 16 + 8 < p.head_dim) *reinterpret_cast<uint32_t*>(o + ks * 16 + 8 + 2 * t) = b;
                         }
                     }
                 }
-                __syncthreads();
-                const int d4s = min(S::kPartCols, p.head_dim - d0) / 4;
-                for (int i = tid; i < heads * d4s; i += T) {
-                    const int hd = i / d4s, d = (i - hd * d4s) * 4;
-                    const float* at = part_s + hd * S::kPartStride;
-                    float mk[W], top = kNegInf;
+            }
+        } else {
+            // A piece: the last one to the warp's ring, whose copies are all consumed.
+            float* const o = final ? reinterpret_cast<float*>(ring_p) : first_piece(w);
+            float2* const ml = s_ml[2 * w + (final ? 1 : 0)];
 #pragma unroll
-                    for (int k = 0; k < W; ++k) {
-                        mk[k] = at[k * 8 * S::kPartStride + S::kPartCols];
-                        top = fmaxf(top, mk[k]);
-                    }
-                    float sum = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int k = 0; k < W; ++k) {
-                        const float* a = at + k * 8 * S::kPartStride;
-                        if (mk[k] != kNegInf) {
-                            const float e = exp2f(mk[k] - top);
-                            const float4 v = *reinterpret_cast<const float4*>(a + d);
-                            sum += a[S::kPartCols + 1] * e;
-                            o.x += v.x * e;
-                            o.y += v.y * e;
-                            o.z += v.z * e;
-                            o.w += v.w * e;
+                for (int j = 0; j < 2; ++j) {
+                    const int hd = nb * 8 + 2 * t + j;
+                    if (hd < nh) {
+                        if (g == 0) ml[hd] = make_float2(m[nb][j], l[nb][j]);
+                        // Column d of head hd at d ^ 8 t: the four heads a store covers lie in different banks.
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) {
+                            const int d0 = ks * 16 + (FP8 ? 2 * g : g), d1 = FP8 ? d0 + 1 : d0 + 8;
+                            o[hd * DT + (d0 ^ 8 * t)] = acc[ks][nb][j];
+                            o[hd * DT + (d1 ^ 8 * t)] = acc[ks][nb][j + 2];
                         }
                     }
-                    const int hh = nb * 8 + hd;
-                    if (whole) {
-                        store(hh, d0 + d, o, top, sum);
-                    } else {
-                        *reinterpret_cast<float4*>(p.part + (piece * (NB * 8) + hh) * DT + d0 + d) = o;
-                        if (d0 + d == 0)
-                            *reinterpret_cast<float2*>(p.part_ml + (piece * (NB * 8) + hh) * 2) = make_float2(top, sum);
-                    }
                 }
-            }
-        }
-        if (!whole) {
-            const int64_t row_first = f0 + done - s;                 // the row's place in the list
-            const int c1 = static_cast<int>(row_first / quota), c2 = static_cast<int>((row_first + ns - 1) / quota);
-            __threadfence();
-            __syncthreads();
-            uint32_t* ticket = p.ticket + c1 * p.qtiles + qt;
-            if (tid == 0) {
-                const uint32_t old = atomicAdd(ticket, 1u);
-                s_last = old == static_cast<uint32_t>(c2 - c1);
-                if (s_last) *ticket = 0u;                            // zero again for the next call
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                const int d4s = p.head_dim / 4;
-                for (int i = tid; i < nh * d4s; i += T) {
-                    const int hd = i / d4s, d = (i - hd * d4s) * 4;
-                    auto piece_of = [&](int c) {
-                        return ((static_cast<int64_t>(c) * p.qtiles + qt) * 2 + (c == c1 ? 1 : 0)) * (NB * 8) + hd;
-                    };
-                    float top = kNegInf;
-#pragma unroll 4
-                    for (int c = c1; c <= c2; ++c) top = fmaxf(top, __ldcg(p.part_ml + piece_of(c) * 2));
-                    float sum = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = c1; c <= c2; ++c) {
-                        const int64_t at = piece_of(c);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part + at * DT + d));
-                        const float e = ml.x == kNegInf ? 0.f : exp2f(ml.x - top);
-                        sum += ml.y * e;
-                        o.x += v.x * e;
-                        o.y += v.y * e;
-                        o.z += v.z * e;
-                        o.w += v.w * e;
-                    }
-                    store(hd, d, o, top, sum);
-                }
-            }
+            if (lane == 0) s_piece[2 * w + (final ? 1 : 0)] = {1, r, h, s, seg, ns, at, v_scale};
         }
 
-        done += seg;
-        s += seg;
-        if (s == ns && done < cnt) {
-            s = 0;
-            if (++h == p.kv_heads) {
-                h = 0;
-                do ++r;
-                while (r < p.requests && attn_slices<TS>(p, len_of(r)) == 0);
-                if (r >= p.requests) break;
+        left -= seg;
+        at += seg;
+        s = 0;                                                       // a part that goes on, goes on with a new row
+        r = next_r;
+        h = next_h;
+        if (!more) break;
+    }
+    // After a timed-out wait: give this warp's other copies in flight the same time to land.
+    if (!ok)
+        for (int i = 0; i < E && wait_phase(bars + take_at * 8, phase); ++i) next_entry();
+    __syncthreads();
+
+    // ---- the warps' pieces, joined row by row ----
+    auto store = [&](int r, int hk, int hd, int d, float4 o, float top, float sum, float scale) {
+        const int64_t row = attn_row(p, r), head = static_cast<int64_t>(hk) * p.group + head0 + hd;
+        const float inv = sum == 0.f ? 0.f : scale / sum;
+        *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * p.head_dim + d) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (p.lse && d == 0) p.lse[row * p.q_heads + head] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
+    };
+    const int d4s = p.head_dim / 4, items = nh * d4s;
+    // Every warp finds the rows among the pieces by itself: lane i holds piece i.
+    Piece own = {0, -1, -1, 0, 0, 0, 0, 1.f};
+    if (lane < 2 * W) own = s_piece[lane];
+    const uint32_t pieces = __ballot_sync(0xffffffffu, own.valid != 0);
+    uint32_t starts;                      // the first piece of each row
+    {
+        const uint32_t before = pieces & ((1u << lane) - 1u);
+        const int prev = before ? 31 - __clz(before) : 0;
+        const int pr = __shfl_sync(0xffffffffu, own.r, prev), ph = __shfl_sync(0xffffffffu, own.h, prev);
+        starts = __ballot_sync(0xffffffffu, own.valid != 0 && (!before || pr != own.r || ph != own.h));
+    }
+    auto piece_at = [&](int i) {
+        Piece a;
+        a.valid = 1;
+        a.r = __shfl_sync(0xffffffffu, own.r, i);
+        a.h = __shfl_sync(0xffffffffu, own.h, i);
+        a.s = __shfl_sync(0xffffffffu, own.s, i);
+        a.seg = __shfl_sync(0xffffffffu, own.seg, i);
+        a.ns = __shfl_sync(0xffffffffu, own.ns, i);
+        a.at = __shfl_sync(0xffffffffu, own.at, i);
+        a.v_scale = __shfl_sync(0xffffffffu, own.v_scale, i);
+        return a;
+    };
+    Piece before = {}, after = {};        // the rows that go on in other CTAs: one from before, one after
+    constexpr int UW = (H * DT / 4 + T - 1) / T;                     // units of 32 items that a warp takes of a row
+#pragma unroll 1
+    for (uint32_t rest = starts; rest;) {
+        const int i = __ffs(rest) - 1;
+        rest &= rest - 1;
+        const uint32_t of = pieces & (0xffffffffu << i) & (rest ? (1u << (__ffs(rest) - 1)) - 1u : 0xffffffffu);
+        // The row's pieces: i, i + 2, .. the last ones of consecutive warps, and j, the last or the first of the
+        // warp where the row (or the range) ends.
+        const int j = 31 - __clz(of), n = __popc(of);
+        const Piece a = piece_at(i);
+        const int reach = __shfl_sync(0xffffffffu, own.s + own.seg, j);
+        const bool whole = a.s == 0 && reach == a.ns;
+        if (!whole) (a.s == 0 ? after : before) = a;
+        const int64_t piece = static_cast<int64_t>(blockIdx.x) * 2 + (a.s == 0 ? 1 : 0);
+        // Piece j first: it may have to come from the workspace, all of this warp's share at once.
+        float4 tail[UW];
+#pragma unroll
+        for (int u = 0; u < UW; ++u) {
+            const int x = u * T + tid, hd = x / d4s, d = (x - hd * d4s) * 4;
+            const float* from = j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * kAttnRing) : first_piece(j >> 1);
+            if (x < items) tail[u] = *reinterpret_cast<const float4*>(from + hd * DT + (d ^ (hd >> 1 & 3) * 8));
+        }
+#pragma unroll
+        for (int u = 0; u < UW; ++u) {
+            const int x = u * T + tid;
+            if (x >= items) break;
+            const int hd = x / d4s, d = (x - hd * d4s) * 4;
+            const int place = hd * DT + (d ^ (hd >> 1 & 3) * 8);
+            const float2 ml_j = s_ml[j][hd];
+            float2 ml[W - 1];
+            float top = ml_j.x;
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                ml[k] = k < n - 1 ? s_ml[i + 2 * k][hd] : make_float2(kNegInf, 0.f);
+                top = fmaxf(top, ml[k].x);
+            }
+            const float base = top == kNegInf ? 0.f : top;
+            float e = exp2_ftz(ml_j.x - base);
+            float sum = ml_j.y * e;
+            float4 o = make_float4(tail[u].x * e, tail[u].y * e, tail[u].z * e, tail[u].w * e);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+                if (k < n - 1) {
+                    const float4 v = *reinterpret_cast<const float4*>(smem + ((i >> 1) + k) * kAttnRing + place * 4);
+                    e = exp2_ftz(ml[k].x - base);
+                    sum += ml[k].y * e;
+                    o.x += v.x * e;
+                    o.y += v.y * e;
+                    o.z += v.z * e;
+                    o.w += v.w * e;
+                }
+            if (whole) {
+                store(a.r, a.h, hd, d, o, top, sum, a.v_scale);
+            } else {
+                *reinterpret_cast<float4*>(p.part + (piece * H + hd) * DT + d) = o;
+                if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (piece * H + hd) * 2) = make_float2(top, sum);
             }
         }
     }
-    copy_wait<0>();
+    if (!before.valid && !after.valid) return;
+
+    // ---- rows cut between CTAs: the CTA that arrives last joins their pieces ----
+    __threadfence();
+    __syncthreads();
+    // The first and last CTA of the row from before (lanes 0 and 1), of the one after (lanes 2 and 3).
+    const Piece cut = lane < 2 ? before : after;
+    const int64_t place = f0 + cut.at - cut.s + (lane & 1 ? cut.ns - 1 : 0);
+    const int ends = total >> 31 ? static_cast<int>(attn_div(place, quota))
+                                 : static_cast<int>(static_cast<uint32_t>(place) / static_cast<uint32_t>(quota));
+    const int from0 = __shfl_sync(0xffffffffu, ends, 0), to0 = __shfl_sync(0xffffffffu, ends, 1);
+    const int from1 = __shfl_sync(0xffffffffu, ends, 2), to1 = __shfl_sync(0xffffffffu, ends, 3);
+    if (lane == 0 && w < 2) {
+        int last = 0;
+        if (w == 0 ? before.valid : after.valid) {
+            uint32_t* ticket = p.ticket + (w == 0 ? from0 : from1) * p.qtiles + qt;
+            last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(w == 0 ? to0 - from0 : to1 - from1);
+            if (last) *ticket = 0u;                                  // zero again for the next call
+        }
+        s_last[w] = last;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        if (!s_last[k]) continue;
+        __threadfence();
+        const int r = k == 0 ? before.r : after.r, hk = k == 0 ? before.h : after.h;
+        const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1;
+        const float scale = k == 0 ? before.v_scale : after.v_scale;
+#pragma unroll 1
+        for (int x = tid; x < items; x += T) {
+            const int hd = x / d4s, d = (x - hd * d4s) * 4;
+            // Piece 1 of the first CTA, piece 0 of the others. The maximum runs along, so the loads of the pieces do
+            // not wait for each other.
+            const int64_t head = (static_cast<int64_t>(from) * p.qtiles + qt) * 2 * H + hd;
+            const float* v_at = p.part + head * DT + d;
+            const float* ml_at = p.part_ml + head * 2;
+            const int64_t step = static_cast<int64_t>(p.qtiles) * 2 * H;
+            float top = kNegInf, sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            int64_t at = static_cast<int64_t>(H);
+#pragma unroll 8
+            for (int c = from; c <= to; ++c) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(ml_at + at * 2));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(v_at + at * DT));
+                at = (c - from + 1) * step;
+                const float next = fmaxf(top, ml.x), base = next == kNegInf ? 0.f : next;
+                const float e = exp2_ftz(top - base), f = exp2_ftz(ml.x - base);
+                sum = sum * e + ml.y * f;
+                o.x = o.x * e + v.x * f;
+                o.y = o.y * e + v.y * f;
+                o.z = o.z * e + v.z * f;
+                o.w = o.w * e + v.w * f;
+                top = next;
+            }
+            store(r, hk, hd, d, o, top, sum, scale);
+        }
+    }
 }
 
 }  // namespace gemv

@@ -140,8 +140,8 @@ def test_attention_query(q_heads, kv_heads, dim, tile, tiles, dim_tile):
     assert (i["head_tile"], i["head_tiles"], i["dim_tile"]) == (tile, tiles, dim_tile)
     assert i["grid"] % tiles == 0 and i["grid"] <= SMS
     assert i["head_tile"] * tiles >= q_heads // kv_heads
-    # two pieces a CTA: outputs, maxima and sums
-    assert i["workspace_bytes"] == 4096 + i["grid"] * 2 * tile * (dim_tile + 2) * 4
+    # two pieces a CTA and one a warp: outputs, maxima and sums
+    assert i["workspace_bytes"] == 4096 + i["grid"] * (2 + i["warps_per_cta"]) * tile * (dim_tile + 2) * 4
 
 
 @pytest.mark.parametrize("args", [(0, 1, 64, 0, SMS), (8, 0, 64, 0, SMS), (7, 2, 64, 0, SMS), (8, 2, 60, 0, SMS),
