@@ -38,6 +38,14 @@ int check_cache(const gemv_kv_cache* c) {
     return GEMV_OK;
 }
 
+// log2 of a power of two, -1 of other sizes.
+int shift_of(int32_t n) {
+    if ((n & (n - 1)) != 0) return -1;
+    int s = 0;
+    while ((1 << s) < n) ++s;
+    return s;
+}
+
 int elem_bytes(const gemv_kv_cache* c) { return c->kind == GEMV_CACHE_FP8 ? 1 : 2; }
 
 int check_rope(const gemv_rope_args* a) {
@@ -86,11 +94,15 @@ void fill_rope(const gemv_rope_args* a, gemv::RopeParams* p) {
     p->rows_f32 = a->rows == GEMV_ROWS_F32;
     p->interleaved = a->pairs == GEMV_PAIRS_INTERLEAVED;
     p->axes = a->axes;
-    // Four pairs at a time where every such group is whole and starts on the boundary of its vector access.
-    const uintptr_t in = p->rows_f32 ? 16 : 8;
-    p->vec = a->head_dim % 8 == 0 && a->rot_dim % 8 == 0 && a->q_stride % 4 == 0 && a->k_stride % 4 == 0 &&
-             a->q_out_stride % 4 == 0 && aligned(a->q, in) && aligned(a->k, in) && aligned(a->q_out, 8) &&
-             (!a->v || (a->v_stride % 4 == 0 && aligned(a->v, in)));
+    // 16-byte reads (eight pairs of BF16 columns, four of FP32 ones) where every such group is whole and every row
+    // starts on the boundary of its reads and writes; else a pair at a time.
+    const int v = p->rows_f32 ? 4 : 8;
+    const uintptr_t out = 2 * static_cast<uintptr_t>(v);
+    p->vec = a->head_dim % (2 * v) == 0 && a->rot_dim % (2 * v) == 0 && a->q_stride % v == 0 && a->k_stride % v == 0 &&
+                     a->q_out_stride % v == 0 && aligned(a->q, 16) && aligned(a->k, 16) && aligned(a->q_out, out) &&
+                     (!a->v || (a->v_stride % v == 0 && aligned(a->v, 16)))
+                 ? v
+                 : 1;
 }
 
 int finish(cudaError_t e) { return e == cudaSuccess ? GEMV_OK : gemv::api_cuda_fail(e); }
@@ -139,6 +151,7 @@ int gemv_block_tables(const gemv_block_tables_args* a, void* stream) {
     p.num_pages = a->num_pages;
     p.table_width = a->table_width;
     p.free_cap = a->free_cap;
+    p.page_shift = shift_of(a->page_size);
     return finish(gemv::launch_tables(p, sm_count, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
 }
 
@@ -169,13 +182,10 @@ int gemv_rope(const gemv_rope_args* a, void* stream) {
     if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
     gemv::RopeParams p = {};
     fill_rope(a, &p);
-    p.vec = p.vec && a->k_out_stride % 4 == 0 && aligned(a->k_out, 8);
-    // k_out as a cache of pages of one token
-    p.kc = static_cast<unsigned char*>(a->k_out);
-    p.page_size = 1;
+    if (a->k_out_stride % p.vec != 0 || !aligned(a->k_out, 2 * static_cast<uintptr_t>(p.vec))) p.vec = 1;
+    p.kc = static_cast<unsigned char*>(a->k_out);           // a cache of pages of one token, token t in page t
     p.page_stride = a->k_out_stride * 2;
     p.head_stride = a->head_dim * 2;
-    p.num_slots = a->tokens;
     return finish(gemv::launch_rope(p, sm_count, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
 }
 
@@ -199,6 +209,7 @@ int gemv_rope_append(const gemv_rope_args* a, const gemv_kv_cache* c, void* stre
     p.v_scale = c->v_scale;
     p.fp8 = c->kind == GEMV_CACHE_FP8;
     p.page_size = c->page_size;
+    p.page_shift = shift_of(c->page_size);
     const int es = elem_bytes(c);
     p.page_stride = c->page_stride * es;
     p.head_stride = c->head_stride * es;
@@ -287,10 +298,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.window = a->window;
     const int64_t reach = static_cast<int64_t>(a->table_width) * c->page_size;
     p.max_len = static_cast<int32_t>(reach < 0x7fffffe0LL ? reach : 0x7fffffe0LL);
-    p.page_shift = -1;
-    if ((c->page_size & (c->page_size - 1)) == 0)
-        for (p.page_shift = 0; (1 << p.page_shift) < c->page_size; ++p.page_shift) {
-        }
+    p.page_shift = shift_of(c->page_size);
     // Tensor copies where a box of at least 8 slots (the swizzle's pattern) divides page and slice.
     const int64_t es = elem_bytes(c);
     int rows = 1;

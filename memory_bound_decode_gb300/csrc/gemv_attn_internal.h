@@ -102,6 +102,7 @@ struct RopeParams {
     int64_t num_slots;
     int32_t tokens, q_heads, kv_heads, head_dim, rot_dim, page_size;
     int32_t rows_f32, interleaved, fp8, axes, vec;
+    int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
 };
 
 cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t s, bool pdl);
@@ -123,6 +124,7 @@ struct TablesParams {
     int32_t* free_next_out;
     int64_t table_stride, max_tokens;
     int32_t requests, page_size, num_pages, table_width, free_cap;
+    int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
 };
 
 cudaError_t launch_tables(const TablesParams& p, int sm_count, cudaStream_t s, bool pdl);

@@ -1,174 +1,254 @@
 // Block tables and slot maps from request lengths.
 //
 // Two running sums over the requests (tokens, new pages) say where each
-// request's tokens and pages begin; after them every token is on its own:
-// its place in the request gives the page, from the request's table row or
-// from the free list. One CTA does both where the tokens are few; otherwise a
-// second kernel with a thread per token follows the first. Bound by latency:
-// a few dependent reads and two block-wide sums.
+// request's tokens and pages begin; after them every token is on its own: its
+// place in the request gives the page, from the request's row of the table or
+// from the free list. Bound by latency: the lengths, a block-wide sum, a page
+// number, its slot.
+//
+// Up to 1,024 requests one launch does it all. Every CTA sums all the requests
+// for itself (cheaper than a second launch that waits for the first: 13.5 us
+// for half a million tokens of 509 requests that way) and fills its share of
+// the slots; the first one writes what belongs to the requests. In a decode
+// step, where no request has more than a few tokens, a thread keeps its
+// request and writes those tokens itself, with nothing to search. More
+// requests, or many tokens with lens and new_lens the same array (which the
+// first CTA then may not write while others read), take two launches.
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "gemv_attn_internal.h"
+#include "gemv_common.cuh"
 
 namespace gemv {
 namespace {
 
-constexpr int kScanThreads = 1024;
+constexpr int kTableThreads = 1024;      // and the requests of one launch
+constexpr int kOneCtaTokens = 4096;      // up to so many tokens a single CTA takes them
+constexpr int kFewTokens = 4;            // a request's tokens that its thread writes itself
 constexpr int kFillThreads = 256;
-constexpr int kFillTokens = 1024;        // tokens of one CTA of the second kernel
+constexpr int kFillTokens = 1024;        // tokens of a CTA of the second launch
 constexpr int kStartsMax = 4096;         // requests whose first tokens fit shared memory there
-constexpr int64_t kOneCtaTokens = 8192;  // up to so many tokens the first kernel does it all
 
-constexpr int64_t kMaxInt = 0x7fffffff;
+constexpr uint32_t kMax = 0x7fffffffu;   // numbers stop here
 
 enum { kServed = 0, kNoPages = 1, kTooLong = 2, kNoRoom = 3, kInvalid = 4 };
 
-__host__ __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// a + b, at most kMax (both at most kMax). Adding so is associative.
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) { return min(a + b, kMax); }
 
-// One token of the step. first_of(r): the first token of request r, for r in 0..requests.
-template <class First>
-__device__ __forceinline__ void fill_token(const TablesParams& p, int64_t tok, int64_t total, First first_of) {
-    int32_t slot = -1, position = 0;
-    if (tok < total) {
-        int lo = 0, hi = p.requests;                        // first_of(lo) <= tok < first_of(hi)
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (first_of(mid) <= tok) lo = mid;
-            else hi = mid;
-        }
-        if (p.status[lo] == kServed) {
-            const int32_t count = p.new_tokens[lo];
-            const int32_t old = p.new_lens[lo] - count;     // lens may be new_lens, already advanced
-            position = old + static_cast<int32_t>(tok - first_of(lo));
-            const int32_t blk = position / p.page_size, have = static_cast<int32_t>(ceil_div(old, p.page_size));
-            int32_t page;
-            if (blk >= have) {
-                page = p.free_pages[p.page_start[lo] + (blk - have)];
-                // the page's first token writes the table (every fresh page has one: it starts behind the old ones)
-                if (position == blk * p.page_size) p.table[lo * p.table_stride + blk] = page;
-            } else {
-                page = p.table[lo * p.table_stride + blk];
-            }
-            if (page >= 0 && page < p.num_pages) slot = page * p.page_size + position - blk * p.page_size;
-        }
-    }
-    p.slots[tok] = slot;
-    p.positions[tok] = position;
+__device__ __forceinline__ int blocks_of(const TablesParams& p, int len) {   // pages that len tokens take
+    return p.page_shift >= 0 ? static_cast<int>((static_cast<uint32_t>(len) + p.page_size - 1) >> p.page_shift)
+                             : len / p.page_size + (len % p.page_size != 0);
+}
+__device__ __forceinline__ int block_at(const TablesParams& p, int position) {
+    return p.page_shift >= 0 ? position >> p.page_shift : position / p.page_size;
 }
 
-// One CTA. FILL: also the tokens.
-template <bool FILL>
-__global__ void __launch_bounds__(kScanThreads) tables_scan_kernel(const __grid_constant__ TablesParams p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ int64_t s_tok[32], s_page[32];
-    __shared__ unsigned long long s_used;                   // pages taken: the largest running sum that was served
-    __shared__ int32_t s_first[FILL ? kScanThreads : 1];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int64_t free_next = *p.free_next;
-    const int64_t avail = free_next < 0 ? 0 : max(static_cast<int64_t>(p.free_cap) - free_next, int64_t(0));
-    const int64_t row_tokens = static_cast<int64_t>(p.table_width) * p.page_size;
-    int64_t tok_carry = 0, page_carry = 0;
-    if (tid == 0) s_used = 0;
-    __syncthreads();                                        // free_next has been read, s_used is zero
-    for (int base = 0; base < p.requests; base += kScanThreads) {
-        const int r = base + tid;
+struct Request {
+    int len, add;                        // as given
+    int state;
+    uint32_t first, page_first;          // tokens and new pages of the requests before it
+};
+struct Sums {
+    uint32_t tokens, pages;              // of the requests so far
+    uint32_t used;                       // pages taken
+};
+
+// The running sums over a chunk of requests, one per thread (`in`: there is one). `sums` holds those of the chunks
+// before and then those up to this one's end. All threads call it.
+__device__ __forceinline__ void sum_chunk(const TablesParams& p, Request& q, bool in, uint32_t avail, Sums& sums) {
+    __shared__ uint32_t s_tok[32], s_page[32], s_used[32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const uint32_t count = q.add > 0 ? q.add : 0;
+    const int64_t end = static_cast<int64_t>(q.len) + q.add;
+    q.state = !in || q.len < 0 || q.add < 0                                   ? kInvalid
+              : end > static_cast<int64_t>(p.table_width) * p.page_size       ? kTooLong
+                                                                              : kServed;
+    uint32_t need = q.state == kServed ? blocks_of(p, q.len + q.add) - blocks_of(p, q.len) : 0;
+    uint32_t tok_all, page_all;
+    // Once; and once more where requests find no room for their tokens, and so take no pages.
+    for (bool again = false;; again = true) {
+        uint32_t tok = count, page = need;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(0xffffffffu, tok, o), b = __shfl_up_sync(0xffffffffu, page, o);
+            if (lane >= o) {
+                tok = sat_add(tok, a);
+                page = sat_add(page, b);
+            }
+        }
+        __syncthreads();                 // s_tok and s_page have been read
+        if (lane == 31) {
+            s_tok[w] = tok;
+            s_page[w] = page;
+        }
+        uint32_t tok_ex = __shfl_up_sync(0xffffffffu, tok, 1), page_ex = __shfl_up_sync(0xffffffffu, page, 1);
+        if (lane == 0) tok_ex = page_ex = 0;
+        __syncthreads();
+        uint32_t t = s_tok[lane], g = s_page[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(0xffffffffu, t, o), b = __shfl_up_sync(0xffffffffu, g, o);
+            if (lane >= o) {
+                t = sat_add(t, a);
+                g = sat_add(g, b);
+            }
+        }
+        tok_all = __shfl_sync(0xffffffffu, t, 31);
+        page_all = __shfl_sync(0xffffffffu, g, 31);
+        const uint32_t tw = __shfl_sync(0xffffffffu, t, max(w - 1, 0)), gw = __shfl_sync(0xffffffffu, g, max(w - 1, 0));
+        q.first = sat_add(sums.tokens, sat_add(tok_ex, w > 0 ? tw : 0));
+        q.page_first = sat_add(sums.pages, sat_add(page_ex, w > 0 ? gw : 0));
+        if (again) break;
+        const bool over = q.state == kServed && count > 0 && sat_add(q.first, count) > p.max_tokens;
+        if (over) {
+            q.state = kNoRoom;
+            need = 0;
+        }
+        if (!__syncthreads_or(over)) break;
+    }
+    const uint32_t pages = sat_add(q.page_first, need);
+    if (q.state == kServed && need > 0 && (pages > avail || pages == kMax)) q.state = kNoPages;
+    const uint32_t used = __reduce_max_sync(0xffffffffu, q.state == kServed && need > 0 ? pages : 0u);
+    if (lane == 0) s_used[w] = used;
+    __syncthreads();
+    sums.used = max(sums.used, __reduce_max_sync(0xffffffffu, s_used[lane]));
+    sums.tokens = sat_add(sums.tokens, tok_all);
+    sums.pages = sat_add(sums.pages, page_all);
+}
+
+__device__ __forceinline__ uint32_t pages_left(const TablesParams& p, int free_next) {
+    return free_next < 0 || free_next > p.free_cap ? 0u : static_cast<uint32_t>(p.free_cap - free_next);
+}
+
+// What belongs to request r (page_start: where its pages begin in the free list; never read where it takes none).
+__device__ __forceinline__ void store_request(const TablesParams& p, int r, const Request& q, int free_next) {
+    p.token_start[r] = static_cast<int32_t>(q.first);
+    p.page_start[r] = q.state != kServed
+                          ? -1
+                          : static_cast<int32_t>(min(static_cast<int64_t>(free_next) + q.page_first, int64_t(kMax)));
+    p.new_lens[r] = q.state == kServed ? q.len + q.add : q.len;
+    p.status[r] = q.state;
+}
+
+// A token of a served request that had `old` tokens: its slot, and the table's entry if it is the first of a page (a
+// page that is new this step has its first token in this step).
+__device__ __forceinline__ void store_token(const TablesParams& p, int64_t tok, int r, int old, int position,
+                                            int page_start) {
+    const int blk = block_at(p, position), have = blocks_of(p, old), in = position - blk * p.page_size;
+    int32_t* const entry = p.table + r * p.table_stride + blk;
+    const int page = blk >= have ? p.free_pages[page_start + (blk - have)] : *entry;
+    if (blk >= have && in == 0) *entry = page;
+    p.slots[tok] = page >= 0 && page < p.num_pages ? page * p.page_size + in : -1;
+    p.positions[tok] = position;
+}
+__device__ __forceinline__ void store_nothing(const TablesParams& p, int64_t tok) {
+    p.slots[tok] = -1;
+    p.positions[tok] = 0;
+}
+
+// The last request whose first token is not behind tok: that token's.
+template <class First>
+__device__ __forceinline__ int request_of(int requests, uint32_t tok, First first) {
+    int lo = 0, hi = requests;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first(mid) <= tok) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Up to kTableThreads requests, any number of CTAs.
+__global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_constant__ TablesParams p) {
+    __shared__ uint32_t s_first[kTableThreads];
+    __shared__ int32_t s_old[kTableThreads], s_start[kTableThreads];   // s_old: -1 if the request was refused
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
+    const int r = threadIdx.x;
+    const bool in = r < p.requests;
+    const int free_next = *p.free_next;
+    Request q = {in ? p.lens[r] : 0, in ? p.new_tokens[r] : 0};
+    Sums sums = {};
+    sum_chunk(p, q, in, pages_left(p, free_next), sums);
+    if (blockIdx.x == 0) {
+        if (in) store_request(p, r, q, free_next);
+        if (r == 0) {
+            p.token_start[p.requests] = static_cast<int32_t>(sums.tokens);
+            *p.free_next_out = free_next + static_cast<int32_t>(sums.used);
+        }
+    }
+    const int start = free_next + static_cast<int32_t>(q.page_first);
+    if (gridDim.x == 1 && !__syncthreads_or(in && q.add > kFewTokens)) {
+        if (in)
+            for (int i = 0; i < q.add; ++i) {
+                const int64_t tok = static_cast<int64_t>(q.first) + i;
+                if (tok >= p.max_tokens) break;
+                if (q.state == kServed) store_token(p, tok, r, q.len, q.len + i, start);
+                else store_nothing(p, tok);
+            }
+        for (int64_t tok = sums.tokens + static_cast<int64_t>(r); tok < p.max_tokens; tok += kTableThreads)
+            store_nothing(p, tok);
+        return;
+    }
+    if (in) {
+        s_first[r] = q.first;
+        s_old[r] = q.state == kServed ? q.len : -1;
+        s_start[r] = start;
+    }
+    __syncthreads();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kTableThreads;
+    for (int64_t tok = static_cast<int64_t>(blockIdx.x) * kTableThreads + r; tok < p.max_tokens; tok += stride) {
+        const int of = request_of(p.requests, static_cast<uint32_t>(tok), [&](int i) { return s_first[i]; });
+        if (tok < sums.tokens && s_old[of] >= 0)
+            store_token(p, tok, of, s_old[of], s_old[of] + static_cast<int>(tok - s_first[of]), s_start[of]);
+        else
+            store_nothing(p, tok);
+    }
+}
+
+// Any number of requests: one CTA for the sums, then the tokens.
+__global__ void __launch_bounds__(kTableThreads) tables_sums_kernel(const __grid_constant__ TablesParams p) {
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
+    const int free_next = *p.free_next;
+    Sums sums = {};
+    for (int base = 0; base < p.requests; base += kTableThreads) {
+        const int r = base + threadIdx.x;
         const bool in = r < p.requests;
-        const int64_t len = in ? p.lens[r] : 0, add = in ? p.new_tokens[r] : 0;
-        const int64_t count = add < 0 ? 0 : add;
-        int64_t tok_incl = count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, tok_incl, o);
-            if (lane >= o) tok_incl += up;
-        }
-        if (lane == 31) s_tok[w] = tok_incl;
-        __syncthreads();
-        int64_t tok_before = tok_carry, all = 0;
-        {
-            int64_t v = s_tok[lane];
-            all = v;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            if (lane >= w) v = 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            tok_before += v;
-        }
-        tok_incl += tok_before;
-        tok_carry += all;
-
-        int state = kServed;
-        if (len < 0 || add < 0) state = kInvalid;
-        else if (len + add > row_tokens) state = kTooLong;
-        else if (count > 0 && tok_incl > p.max_tokens) state = kNoRoom;
-        const int64_t need =
-            state == kServed ? ceil_div(len + count, p.page_size) - ceil_div(len, p.page_size) : 0;
-        int64_t page_incl = need;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, page_incl, o);
-            if (lane >= o) page_incl += up;
-        }
-        if (lane == 31) s_page[w] = page_incl;
-        __syncthreads();
-        {
-            int64_t v = s_page[lane];
-            all = v;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            if (lane >= w) v = 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            page_incl += v + page_carry;
-        }
-        page_carry += all;
-        if (state == kServed && need > 0 && page_incl > avail) state = kNoPages;
-
-        if (in) {
-            const int64_t first = tok_incl - count;
-            const int32_t first32 = static_cast<int32_t>(min(first, kMaxInt));
-            p.token_start[r] = first32;
-            if (FILL && p.requests <= kScanThreads) s_first[r] = first32;
-            // Within the list where the request takes pages; where it takes none, never read.
-            p.page_start[r] =
-                state == kServed ? static_cast<int32_t>(min(free_next + page_incl - need, kMaxInt)) : -1;
-            p.new_lens[r] = static_cast<int32_t>(state == kServed ? len + count : len);
-            p.status[r] = state;
-            if (state == kServed && need > 0) atomicMax(&s_used, static_cast<unsigned long long>(page_incl));
-        }
-        __syncthreads();                                    // s_tok and s_page have been read
+        Request q = {in ? p.lens[r] : 0, in ? p.new_tokens[r] : 0};
+        sum_chunk(p, q, in, pages_left(p, free_next), sums);
+        if (in) store_request(p, r, q, free_next);
     }
-    if (tid == 0) {
-        p.token_start[p.requests] = static_cast<int32_t>(min(tok_carry, kMaxInt));
-        *p.free_next_out = static_cast<int32_t>(free_next + static_cast<int64_t>(s_used));
-    }
-    if constexpr (FILL) {
-        __syncthreads();                                    // status, page_start and new_lens are written
-        const bool near = p.requests <= kScanThreads;
-        for (int64_t tok = tid; tok < p.max_tokens; tok += kScanThreads)
-            fill_token(p, tok, tok_carry,
-                       [&](int r) { return static_cast<int64_t>(near ? s_first[r] : p.token_start[r]); });
+    if (threadIdx.x == 0) {              // behind sum_chunk's barriers: every thread has read free_next
+        p.token_start[p.requests] = static_cast<int32_t>(sums.tokens);
+        *p.free_next_out = free_next + static_cast<int32_t>(sums.used);
     }
 }
 
 __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const __grid_constant__ TablesParams p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ int32_t s_first[kStartsMax + 1];
+    __shared__ int32_t s_first[kStartsMax];
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
     const bool near = p.requests <= kStartsMax;
     if (near)
-        for (int r = threadIdx.x; r <= p.requests; r += kFillThreads) s_first[r] = p.token_start[r];
+        for (int r = threadIdx.x; r < p.requests; r += kFillThreads) s_first[r] = p.token_start[r];
     __syncthreads();
     const int64_t total = p.token_start[p.requests];
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kFillTokens;
 #pragma unroll
     for (int i = 0; i < kFillTokens / kFillThreads; ++i) {
         const int64_t tok = base + i * kFillThreads + threadIdx.x;
-        if (tok < p.max_tokens)
-            fill_token(p, tok, total,
-                       [&](int r) { return static_cast<int64_t>(near ? s_first[r] : p.token_start[r]); });
+        if (tok >= p.max_tokens) break;
+        auto first = [&](int r) { return static_cast<uint32_t>(near ? s_first[r] : p.token_start[r]); };
+        const int of = request_of(p.requests, static_cast<uint32_t>(tok), first);
+        if (tok < total && p.status[of] == kServed) {
+            const int old = p.new_lens[of] - p.new_tokens[of];       // lens may be new_lens, already advanced
+            store_token(p, tok, of, old, old + static_cast<int>(tok - first(of)), p.page_start[of]);
+        } else {
+            store_nothing(p, tok);
+        }
     }
 }
 
@@ -188,11 +268,17 @@ cudaError_t launch(void (*f)(TablesParams), int64_t grid, int threads, const Tab
 
 }  // namespace
 
-cudaError_t launch_tables(const TablesParams& p, int /*sm_count*/, cudaStream_t s, bool pdl) {
-    if (p.max_tokens <= kOneCtaTokens) return launch(tables_scan_kernel<true>, 1, kScanThreads, p, s, pdl);
-    const cudaError_t e = launch(tables_scan_kernel<false>, 1, kScanThreads, p, s, pdl);
+cudaError_t launch_tables(const TablesParams& p, int sm_count, cudaStream_t s, bool pdl) {
+    if (p.requests <= kTableThreads) {
+        if (p.max_tokens <= kOneCtaTokens) return launch(tables_kernel, 1, kTableThreads, p, s, pdl);
+        if (p.lens != p.new_lens && p.free_next != p.free_next_out) {
+            const int64_t ctas = (p.max_tokens + kTableThreads - 1) / kTableThreads;
+            return launch(tables_kernel, ctas < sm_count ? ctas : sm_count, kTableThreads, p, s, pdl);
+        }
+    }
+    const cudaError_t e = launch(tables_sums_kernel, 1, kTableThreads, p, s, pdl);
     if (e != cudaSuccess) return e;
-    return launch(tables_fill_kernel, ceil_div(p.max_tokens, kFillTokens), kFillThreads, p, s, pdl);
+    return launch(tables_fill_kernel, (p.max_tokens + kFillTokens - 1) / kFillTokens, kFillThreads, p, s, pdl);
 }
 
 }  // namespace gemv
