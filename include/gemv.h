@@ -710,8 +710,9 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * Products of BF16 (FP8: codes widened exactly to FP16, and q scaled into FP16
  * by a power of two per head) are summed in FP32, the softmax is kept in FP32;
  * the probabilities meet V as two BF16 parts (FP8: as FP16). requests = 0 is
- * allowed and does nothing. More than 1,024 query heads per key-value head:
- * GEMV_ERR_UNSUPPORTED.
+ * allowed and does nothing. GEMV_ERR_UNSUPPORTED: more than 1,024 query heads
+ * per key-value head; requests * kv_heads * (table_width * page_size / 16 + 2)
+ * above 2,130,706,432.
  */
 typedef struct {
     const void *q;

@@ -256,6 +256,10 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
         !aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(a->table, 4) || !aligned(a->token_start, 4) ||
         !aligned(a->workspace, 16))
         return GEMV_ERR_ALIGN;
+    // The kernel numbers the slices (16 tokens at least) of all rows in 31 bits.
+    const int64_t reach = static_cast<int64_t>(a->table_width) * c->page_size;
+    if (reach > 0x7fffff00LL || static_cast<double>(reach / 16 + 2) * a->requests * c->kv_heads > 0x7f000000)
+        return GEMV_ERR_UNSUPPORTED;
     if (a->requests == 0) return GEMV_OK;
     int sm_count = 0;
     if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
@@ -296,8 +300,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.table_width = a->table_width;
     p.num_pages = c->num_pages;
     p.window = a->window;
-    const int64_t reach = static_cast<int64_t>(a->table_width) * c->page_size;
-    p.max_len = static_cast<int32_t>(reach < 0x7fffffe0LL ? reach : 0x7fffffe0LL);
+    p.max_len = static_cast<int32_t>(reach);
     p.page_shift = shift_of(c->page_size);
     // Tensor copies where a box of at least 8 slots (the swizzle's pattern) divides page and slice.
     const int64_t es = elem_bytes(c);

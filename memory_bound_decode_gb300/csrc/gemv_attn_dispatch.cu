@@ -31,7 +31,7 @@ int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, At
     l->nb = blocks <= 1 ? 1 : blocks <= 2 || most == 2 ? 2 : 4;
     l->qtiles = (blocks + l->nb - 1) / l->nb;
     l->grid = std::max(1, sm_count / l->qtiles) * l->qtiles;
-    if (l->grid > kAttnTickets) return GEMV_ERR_UNSUPPORTED;
+    if (l->grid > kAttnTickets / 2) return GEMV_ERR_UNSUPPORTED;
     const int64_t heads = static_cast<int64_t>(l->grid) * (2 + kAttnWarps) * l->nb * 8;   // pieces of CTAs and warps
     l->workspace_bytes = kAttnTickets * 4 + heads * (2 + l->dt) * 4;
     l->warps = kAttnWarps;

@@ -22,7 +22,7 @@ bool api_encode_pool(CUtensorMap* map, const void* base, bool fp8, const int64_t
 
 // ---- attention ----------------------------------------------------------------
 
-constexpr int kAttnTickets = 1024;        // join counters at the start of the workspace
+constexpr int kAttnTickets = 1024;        // counters at the start of the workspace: rows, then groups of pieces
 constexpr int kAttnMaxGroup = 1024;       // query heads per key-value head
 
 constexpr int kAttnWarps = 8;

@@ -61,12 +61,24 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+// How the L2 is to keep what a copy brings.
+__device__ __forceinline__ uint64_t keep_first_out() {
+    uint64_t r;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(r));
+    return r;
+}
+__device__ __forceinline__ uint64_t keep_normal() {
+    uint64_t r;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(r));
+    return r;
+}
 // One box of the pool's 4-D view (column, slot, head, page).
 __device__ __forceinline__ void copy_box(uint32_t dst, const void* map, int col, int slot, int head, int page,
-                                         uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
-                 :: "r"(dst), "l"(map), "r"(col), "r"(slot), "r"(head), "r"(page), "r"(bar) : "memory");
+                                         uint32_t bar, uint64_t keep) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;"
+                 :: "r"(dst), "l"(map), "r"(col), "r"(slot), "r"(head), "r"(page), "r"(bar), "l"(keep) : "memory");
 }
 // Wait for the barrier's phase, for at most kMbarWaitLimit rounds; false (and the status bit) if they ran out.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
@@ -136,11 +148,16 @@ __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(
 
 }  // namespace attn
 
+__device__ __forceinline__ int attn_cut(const AttnParams& p, int len) {   // to what a row of the table holds
+    if (len <= p.max_len) return len;
+    atomicOr(&g_attn_status, kStatusBadPage);
+    return p.max_len;
+}
 // Tokens of request r that its query can reach: its length, cut to what its
 // row of the table holds (with a status bit); 0 for an empty request, negative
 // for one that has no query row in this call.
 static __device__ __noinline__ int attn_len(const AttnParams& p, int r) {
-    int len = p.lens[r];
+    const int len = p.lens[r];
     if (p.token_start) {
         const int a = p.token_start[r], b = p.token_start[r + 1];
         if (b <= a) return -1;
@@ -149,14 +166,8 @@ static __device__ __noinline__ int attn_len(const AttnParams& p, int r) {
             return -1;
         }
     }
-    if (len > p.max_len) {
-        atomicOr(&g_attn_status, kStatusBadPage);
-        len = p.max_len;
-    }
-    return len;
+    return attn_cut(p, len);
 }
-// a / b, out of line: lists of 2^31 slices are legal, not usual.
-static __device__ __noinline__ int64_t attn_div(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t attn_row(const AttnParams& p, int r) {
     return p.token_start ? static_cast<int64_t>(p.token_start[r + 1]) - 1 : r;
 }
@@ -219,9 +230,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     __shared__ Piece s_piece[2 * W];      // each warp's first and last
     __shared__ float2 s_ml[2 * W][H];     // their maxima and sums
     __shared__ int32_t s_len[T];          // lengths of requests len0 .. len0 + T - 1
-    __shared__ int64_t s_scan[W];
-    __shared__ int32_t s_longest[W];
-    __shared__ int64_t s_off[W];
+    __shared__ int2 s_scan[W];
+    __shared__ int32_t s_off[W];
     __shared__ float s_scales[W][2];      // FP8: scales of k and v of the row that q_raw holds
     __shared__ int32_t s_req[W];
     __shared__ int32_t s_last[2];
@@ -247,44 +257,45 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         s_piece[2 * w].valid = s_piece[2 * w + 1].valid = 0;
     }
     for (int i = lane; i < S::kRaw / 16; i += 32) reinterpret_cast<uint4*>(q_raw)[i] = make_uint4(0, 0, 0, 0);
+    // The table into the L2, a line per thread of the grid (no matter who writes it before this call): a page number
+    // is needed as soon as the lengths are known.
+    const int64_t line = (static_cast<int64_t>(blockIdx.x) * T + tid) * 32;
+    if (line < p.requests * p.table_stride) prefetch_l2(p.table + line);
     __syncwarp();
     pdl_wait_prerequisites();
 
     // ---- the sum of the slices, and (in the first chunk of requests) their running sums ----
-    const int len_first = tid < p.requests ? attn_len(p, tid) : -1;
+    const int len_first = tid >= p.requests ? -1 : p.token_start ? attn_len(p, tid) : attn_cut(p, p.lens[tid]);
     const int n_first = attn_slices<TS>(p, len_first);
     s_len[tid] = len_first;
-    int64_t incl = n_first;
+    int incl = n_first;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
     int longest = __reduce_max_sync(0xffffffffu, n_first);
-    if (lane == 31) {
-        s_scan[w] = incl;
-        s_longest[w] = longest;
-    }
+    if (lane == 31) s_scan[w] = make_int2(incl, longest);
     __syncthreads();
-    int64_t carry = 0;
+    int carry = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        if (i < w) incl += s_scan[i];
-        carry += s_scan[i];
-        longest = max(longest, s_longest[i]);
+        const int2 of = s_scan[i];
+        if (i < w) incl += of.x;
+        carry += of.x;
+        longest = max(longest, of.y);
     }
-    int64_t total = carry;
+    int total = carry;
     if (p.requests > T) {
-        int64_t more = 0;
+        int more = 0;
 #pragma unroll 1
         for (int r = T + tid; r < p.requests; r += T) more += attn_slices<TS>(p, attn_len(p, r));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+        more = __reduce_add_sync(0xffffffffu, more);
         __syncthreads();
-        if (lane == 0) s_scan[w] = more;
+        if (lane == 0) s_scan[w].x = more;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < W; ++i) total += s_scan[i];
+        for (int i = 0; i < W; ++i) total += s_scan[i].x;
     }
 
     // Requests without a visible token: zeros (nothing to average), from the CTA whose turn it is.
@@ -298,19 +309,18 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     }
 
     // ---- the CTA's range f0 .. f0 + cnt of the list, this warp's part of it, and the requests the parts begin in ----
-    total *= p.kv_heads;
-    // At least a slice per warp; and rows of up to four per warp are better not cut between CTAs: the last of four
-    // slices comes 2 us after the first, a join across CTAs takes 4.
-    const int least = max(W, longest <= 4 * W ? longest : 0);
-    const int64_t quota = max(total >> 31 ? attn_div(total + ctas - 1, ctas)
-                                          : static_cast<int64_t>((static_cast<uint32_t>(total) + ctas - 1) / ctas),
-                              static_cast<int64_t>(least));
-    const int64_t f0 = cta * quota;
+    total *= p.kv_heads;                                             // below 2^31: checked by the host
+    // At least a slice per warp. Rows of up to two per warp are better not cut between CTAs, and of up to four if
+    // that leaves work for a quarter of the CTAs: the slices of a warp come 1.3 us after each other, a join across
+    // CTAs takes 4 (8 x 1,000 tokens: 12.6 us against 16.0; 1 x 1,000: 11.9 against 10.3).
+    const bool uncut = longest <= 2 * W || (longest <= 4 * W && total / longest * 4 >= ctas);
+    const int quota = max((total + ctas - 1) / ctas, max(W, uncut ? longest : 0));
+    const int f0 = cta * quota;                                      // below total + grid * quota
     if (f0 >= total) return;
-    const int cnt = static_cast<int>(min(quota, total - f0));
+    const int cnt = min(quota, total - f0);
     const int part = (cnt + W - 1) / W;
-    auto claim = [&](int r, int n, int64_t end) {                    // `end`: slices up to request r, a head
-        const int64_t lo = (end - n) * p.kv_heads - f0, hi = end * p.kv_heads - f0;
+    auto claim = [&](int r, int n, int end) {                        // `end`: slices up to request r, a head
+        const int lo = (end - n) * p.kv_heads - f0, hi = end * p.kv_heads - f0;
 #pragma unroll 1
         for (int i = 0; i < W && n > 0; ++i)
             if (lo <= i * part && i * part < hi) {
@@ -327,19 +337,19 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
         __syncthreads();                                             // s_scan and s_len have been read
-        if (lane == 31) s_scan[w] = incl;
+        if (lane == 31) s_scan[w].x = incl;
         s_len[tid] = len;
         len0 = base;
         __syncthreads();
-        int64_t before = carry;
+        int before = carry;
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-            if (i < w) before += s_scan[i];
-            carry += s_scan[i];
+            if (i < w) before += s_scan[i].x;
+            carry += s_scan[i].x;
         }
         claim(base + tid, n, before + incl);
     }
@@ -351,8 +361,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     int h = 0, s = 0;
     if (left > 0) {
         const int ns0 = max(1, attn_slices<TS>(p, len_of(r)));
-        h = s_off[w] >> 31 ? static_cast<int>(attn_div(s_off[w], ns0)) : static_cast<int>(s_off[w]) / ns0;
-        s = static_cast<int>(s_off[w] - static_cast<int64_t>(h) * ns0);
+        h = s_off[w] / ns0;
+        s = s_off[w] - h * ns0;
     }
 
     // ---- queries of a row, as they come, into q_raw ----
@@ -384,6 +394,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     const uint32_t bars = smem_addr(s_bar) + static_cast<uint32_t>(w) * E * 8;
     const int mine = left;                // slices of this warp
     const int chunks = p.head_dim * (FP8 ? 1 : 2) / 16;
+        // K and V that no other CTA reads leave the L2 first where pieces of rows wait in it (wide heads in groups of 16:
+    // 70.4 -> 68.0 us); elsewhere that costs up to 4% of the stream.
+    const uint64_t keep = !S::kFirstShared && p.qtiles == 1 ? keep_first_out() : keep_normal();
     int issued = 0, slot_at = 0;          // slices (their K), and the next entry's place in the ring
     Mask valid_of = 0;                    // lane i: the visible tokens of slice i (modulo 32)
     int64_t off = 0;                      // of the slice whose K went out last, lane i: byte offset of token i;
@@ -504,7 +517,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 __syncwarp();
                 if (lane < per_slice * LINES)
                     copy_box(dst + lane % LINES * TS * 128 + lane / LINES * box * LB, kIsK ? &p.kmap : &p.vmap,
-                             lane % LINES * (FP8 ? 128 : 64), box_in, box_h, box_page, bar);
+                             lane % LINES * (FP8 ? 128 : 64), box_in, box_h, box_page, bar, keep);
             } else {
                 copy_rows(kIsK ? p.kc : p.vc, dst);
                 copies_arrive(bar);
@@ -1012,60 +1025,129 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     if (!before.valid && !after.valid) return;
 
     // ---- rows cut between CTAs: the CTA that arrives last joins their pieces ----
+    //
+    // A row of more than kJoin pieces is joined in groups first, each by the last of its CTAs to arrive, and the
+    // groups' results by the last group. Piece 1 of a row's first CTA, piece 0 of the others; a group's result takes
+    // the place of its last piece.
+    constexpr int kJoin = 32;
     __threadfence();
     __syncthreads();
     // The first and last CTA of the row from before (lanes 0 and 1), of the one after (lanes 2 and 3).
     const Piece cut = lane < 2 ? before : after;
-    const int64_t place = f0 + cut.at - cut.s + (lane & 1 ? cut.ns - 1 : 0);
-    const int ends = total >> 31 ? static_cast<int>(attn_div(place, quota))
-                                 : static_cast<int>(static_cast<uint32_t>(place) / static_cast<uint32_t>(quota));
+    const int ends = (f0 + cut.at - cut.s + (lane & 1 ? cut.ns - 1 : 0)) / quota;
     const int from0 = __shfl_sync(0xffffffffu, ends, 0), to0 = __shfl_sync(0xffffffffu, ends, 1);
     const int from1 = __shfl_sync(0xffffffffu, ends, 2), to1 = __shfl_sync(0xffffffffu, ends, 3);
+    // One more arrival at a counter; whether it is the last of `all`, with the counter zero again for the next call.
+    auto arrive = [&](uint32_t* ticket, int all) {
+        const bool last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(all - 1);
+        if (last) *ticket = 0u;
+        return last;
+    };
+    uint32_t* const of_rows = p.ticket + qt;
+    enum { kWait, kLast, kGroups };
     if (lane == 0 && w < 2) {
-        int last = 0;
+        int state = kWait;
         if (w == 0 ? before.valid : after.valid) {
-            uint32_t* ticket = p.ticket + (w == 0 ? from0 : from1) * p.qtiles + qt;
-            last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(w == 0 ? to0 - from0 : to1 - from1);
-            if (last) *ticket = 0u;                                  // zero again for the next call
+            const int from = w == 0 ? from0 : from1, n = (w == 0 ? to0 : to1) - from + 1;
+            state = n > kJoin ? kGroups : arrive(of_rows + from * p.qtiles, n) ? kLast : kWait;
         }
-        s_last[w] = last;
+        s_last[w] = state;
     }
     __syncthreads();
+
+    // Joins `count` pieces, those of cta_of(0), cta_of(1), ..: B at a time, all of whose loads are in flight together.
+    float top[UW], sum[UW];
+    float4 o[UW];
+    auto join = [&](auto batch, int from, int count, auto cta_of) {
+        constexpr int B = decltype(batch)::value;
+#pragma unroll
+        for (int u = 0; u < UW; ++u) {
+            top[u] = kNegInf;
+            sum[u] = 0.f;
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int b0 = 0; b0 < count; b0 += B) {
+            float2 ml[B][UW];
+            float4 v[B][UW];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int c = cta_of(b0 + b);
+                const int64_t at = ((static_cast<int64_t>(c) * p.qtiles + qt) * 2 + (c == from ? 1 : 0)) * H;
+#pragma unroll
+                for (int u = 0; u < UW; ++u) {
+                    const int x = u * T + tid, hd = x / d4s, d = (x - hd * d4s) * 4;
+                    ml[b][u] = make_float2(kNegInf, 0.f);
+                    if (b0 + b < count && x < items) {
+                        ml[b][u] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (at + hd) * 2));
+                        v[b][u] = __ldcg(reinterpret_cast<const float4*>(p.part + (at + hd) * DT + d));
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int u = 0; u < UW; ++u)
+                    if (ml[b][u].x != kNegInf) {
+                        const float next = fmaxf(top[u], ml[b][u].x);
+                        const float e = exp2_ftz(top[u] - next), f = exp2_ftz(ml[b][u].x - next);
+                        sum[u] = sum[u] * e + ml[b][u].y * f;
+                        o[u].x = o[u].x * e + v[b][u].x * f;
+                        o[u].y = o[u].y * e + v[b][u].y * f;
+                        o[u].z = o[u].z * e + v[b][u].z * f;
+                        o[u].w = o[u].w * e + v[b][u].w * f;
+                        top[u] = next;
+                    }
+        }
+    };
+    auto store_row = [&](int r, int hk, float scale) {
+#pragma unroll
+        for (int u = 0; u < UW; ++u) {
+            const int x = u * T + tid, hd = x / d4s;
+            if (x < items) store(r, hk, hd, (x - hd * d4s) * 4, o[u], top[u], sum[u], scale);
+        }
+    };
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
+        if (s_last[k] != kLast) continue;
+        __threadfence();
+        const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1;
+        join(std::integral_constant<int, 16 / UW>{}, from, to - from + 1, [&](int b) { return from + b; });
+        store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
+    }
+    if (s_last[0] != kGroups && s_last[1] != kGroups) return;
+    const bool big[2] = {s_last[0] == kGroups, s_last[1] == kGroups};
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        if (!(k == 0 ? big[0] : big[1])) continue;
+        const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1, n = to - from + 1;
+        const int g = n <= 64 ? 8 : n <= 256 ? 16 : 32, groups = (n + g - 1) / g;
+        const int begin = from + (cta - from) / g * g, end = min(begin + g - 1, to);
+        // Groups are counted at their last CTA, which no other row's group ends at.
+        __syncthreads();                                             // s_last has been read
+        if (tid == 0) s_last[k] = arrive(p.ticket + kAttnTickets / 2 + end * p.qtiles + qt, end - begin + 1);
+        __syncthreads();
         if (!s_last[k]) continue;
         __threadfence();
-        const int r = k == 0 ? before.r : after.r, hk = k == 0 ? before.h : after.h;
-        const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1;
-        const float scale = k == 0 ? before.v_scale : after.v_scale;
-#pragma unroll 1
-        for (int x = tid; x < items; x += T) {
-            const int hd = x / d4s, d = (x - hd * d4s) * 4;
-            // Piece 1 of the first CTA, piece 0 of the others. The maximum runs along, so the loads of the pieces do
-            // not wait for each other.
-            const int64_t head = (static_cast<int64_t>(from) * p.qtiles + qt) * 2 * H + hd;
-            const float* v_at = p.part + head * DT + d;
-            const float* ml_at = p.part_ml + head * 2;
-            const int64_t step = static_cast<int64_t>(p.qtiles) * 2 * H;
-            float top = kNegInf, sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            int64_t at = static_cast<int64_t>(H);
-#pragma unroll 8
-            for (int c = from; c <= to; ++c) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(ml_at + at * 2));
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(v_at + at * DT));
-                at = (c - from + 1) * step;
-                const float next = fmaxf(top, ml.x), base = next == kNegInf ? 0.f : next;
-                const float e = exp2_ftz(top - base), f = exp2_ftz(ml.x - base);
-                sum = sum * e + ml.y * f;
-                o.x = o.x * e + v.x * f;
-                o.y = o.y * e + v.y * f;
-                o.z = o.z * e + v.z * f;
-                o.w = o.w * e + v.w * f;
-                top = next;
-            }
-            store(r, hk, hd, d, o, top, sum, scale);
+        using Few = std::integral_constant<int, UW == 4 ? 2 : 8 / UW>;
+        join(Few{}, from, end - begin + 1, [&](int b) { return begin + b; });
+        __syncthreads();                                             // every thread has read the group's pieces
+#pragma unroll
+        for (int u = 0; u < UW; ++u) {
+            const int x = u * T + tid, hd = x / d4s, d = (x - hd * d4s) * 4;
+            if (x >= items) break;
+            const int64_t at = (static_cast<int64_t>(end) * p.qtiles + qt) * 2 * H + hd;
+            *reinterpret_cast<float4*>(p.part + at * DT + d) = o[u];
+            if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top[u], sum[u]);
         }
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) s_last[k] = arrive(of_rows + from * p.qtiles, groups);
+        __syncthreads();
+        if (!s_last[k]) continue;
+        __threadfence();
+        join(Few{}, -1, groups, [&](int b) { return min(from + (b + 1) * g - 1, to); });
+        store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
     }
 }
 
