@@ -272,6 +272,9 @@ def describe(workload: str):
     m = re.fullmatch(r"tail:(\d+)x(\d+)", workload)
     if m:
         return "single", [int(m.group(1))], int(m.group(2)), 1
+    m = re.fullmatch(r"attn_step:B(\d+):L(\d+)", workload)
+    if m:
+        return "attn", None, int(m.group(2)), int(m.group(1))
     raise SystemExit(f"unknown workload {workload}")
 
 
@@ -418,6 +421,59 @@ class StepWorkload:
                 "l2": f"inputs larger than L2: {self.data.weight_bytes() / 1e9:.2f} GB of weights per step"}
 
 
+class AttentionWorkload(StepWorkload):
+    """The attention half of a decode step (attn_step:B<b>:L<tokens>, "f8:" for
+    an FP8 cache) replayed as one CUDA graph."""
+
+    def __init__(self, device, context, batch, fp8=False):
+        from memory_bound_decode_gb300 import workloads as wl
+        self.spec = wl.decode_step_spec()
+        self.data = wl.AttentionStep(self.spec, context, batch, device=device, cache="fp8" if fp8 else "bf16")
+        self.data.run()            # sets the library up, outside the capture
+        self.data.capture()
+        self.weights, self.w4, self.fp8 = "bf16", False, fp8
+        self.bytes_per_step = self.data.algorithmic_bytes()
+        self.launches_per_step = self.data.launches
+        self.x, self.B, self.context = None, batch, context
+
+    def step(self, i: int, stream, x=None) -> None:
+        self.data.launch()
+
+    def config(self) -> dict:
+        return {"workload": "attention half of a decode step: block tables + 32 x {QKV 6144x4096, rotary + cache "
+                            f"write, attention over {self.context} + 1 tokens of {self.B} requests, o 4096x4096}}, "
+                            f"BF16 weights, {'FP8' if self.fp8 else 'BF16'} cache, one CUDA graph",
+                "launches_per_step": self.launches_per_step,
+                "l2": f"inputs larger than L2: {self.bytes_per_step / 1e9:.2f} GB per step"}
+
+    def e2e(self, steps: int, stream) -> dict:
+        """Every layer's x in from pinned host memory, the step, every layer's
+        output back, waited for."""
+        import torch
+        xs = [(d["x"], d["x"].cpu().pin_memory()) for d in self.data.layers]
+        os_ = [(torch.empty(d["o"].shape, dtype=d["o"].dtype).pin_memory(), d["o"]) for d in self.data.layers]
+
+        def once():
+            for dev, host in xs:
+                dev.copy_(host, non_blocking=True)
+            self.data.launch()
+            for host, dev in os_:
+                host.copy_(dev, non_blocking=True)
+            stream.synchronize()
+        n = max(5, min(steps, 200))
+        with torch.cuda.stream(stream):
+            for _ in range(5):
+                once()
+            t0 = time.perf_counter()
+            for _ in range(n):
+                once()
+            el = time.perf_counter() - t0
+        return {"value": round(self.bytes_per_step * n / el / 1e9, 2), "unit": UNIT,
+                "h2d_bytes_per_step": sum(h.numel() * h.element_size() for _, h in xs),
+                "d2h_bytes_per_step": sum(h.numel() * h.element_size() for h, _ in os_),
+                "us_per_step": round(el / n * 1e6, 3), "steps": n}
+
+
 # ----------------------------------------------------------------------------- our arm
 
 TARGETS = {"down_proj": 0.85, "gate_up": 0.85, "decode_step": 0.80}   # fraction of HBM peak
@@ -558,6 +614,8 @@ def time_e2e(torch, binding, wk, steps: int, stream) -> dict | None:
     gemv_bf16_multi_host_io, or gemv_plan_launch_host_io (the decode step, and
     a one-projection plan for quantised weights)."""
     sh = stream.cuda_stream
+    if isinstance(wk, AttentionWorkload):
+        return wk.e2e(steps, stream)
     if isinstance(wk, StepWorkload):
         d = wk.data
         x_host = d.x_arena.cpu().pin_memory()
@@ -618,6 +676,10 @@ def make_workload(torch, name: str, device, l2: int):
     base, cuda_cores = split_cc(base)
     base, fp8 = split_f8(base)
     _, w4 = split_w4(base)
+    if kind == "attn":
+        if rms_eps is not None or streamk or cuda_cores or w4:
+            raise SystemExit("attn_step: takes no prefix but f8: and no suffix")
+        return AttentionWorkload(device, K, B, fp8)
     if kind == "step":
         return StepWorkload(device, torch.cuda.Stream(), rms_eps, streamk,
                             "int4" if w4 else "fp8" if fp8 else "bf16", batch=B)
@@ -704,7 +766,8 @@ def run_ours(args) -> dict:
     peak, peak_kind = load_peaks()
     achieved = wk.bytes_per_step / (seconds / steps) / 1e9 if kind == "step" else \
         wk.bytes_per_step / per_launch_s / 1e9
-    family = family_of(wk)
+    attn = isinstance(wk, AttentionWorkload)
+    family = "fma" if attn else family_of(wk)
     launch = None
     if kind == "single":
         sms = props.multi_processor_count
@@ -729,7 +792,7 @@ def run_ours(args) -> dict:
         "us_per_call": round(per_launch_s * 1e6, 3),
         "us_isolated": round(t["isolated_s"] * 1e6, 3),
         "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
-        "dtype": {"w4": "u4 weights (bf16 group scales), bf16 x, fp32 accumulate",
+        "dtype": "bf16 in, fp32 accumulate" + (", e4m3 cache" if wk.fp8 else "") if attn else {"w4": "u4 weights (bf16 group scales), bf16 x, fp32 accumulate",
                   "f8": "e4m3 weights (fp32 row scales), bf16 x, fp32 accumulate"}.get(family, "bf16 in, fp32 accumulate"),
         "data": "synthetic (seeded N(0,0.02^2) weights, N(0,1) x)",
         "config": dict(wk.config(), parallelism="1 GPU",
@@ -741,7 +804,8 @@ def run_ours(args) -> dict:
                      "frac": round(achieved / peak, 4), "traffic": traffic,
                      "peak_kind": f"{peak_kind} copy (MEASURED_PEAKS hbm_gbs, burst)"
                      if peak_kind == "measured" else "fallback 6.8 TB/s",
-                     "kernel": ("gemv_w4_kernel (INT4 codes, BF16 tensor cores)" if family == "w4"
+                     "kernel": ("attn_decode_kernel and the projections' kernels" if attn
+                                else "gemv_w4_kernel (INT4 codes, BF16 tensor cores)" if family == "w4"
                                 else "gemv_fp8_kernel (E4M3 codes, BF16 tensor cores)" if family == "f8"
                                 else "gemv_streamk_kernel (CUDA cores, one-wave grid)" if family == "sk"
                                 else "gemv_tc_kernel (tcgen05, accumulator in tensor memory)" if family == "tc"
@@ -788,6 +852,8 @@ def oracle_sample(workload: str, rows_cap: int | None = None):
     kind, rows, K, B = describe(workload)
     if kind == "step":
         rows, K, B = [4096], 14336, 1      # the step's down projection stands in
+    if kind == "attn":
+        rows, K = [4096], 4096             # the step's output projection stands in: the oracle has no attention
     N = sum(rows)
     n = N if rows_cap is None else max(1, min(N, rows_cap))
     ldw = inputs.padded_ldw(K)
@@ -831,6 +897,8 @@ def cpu_baseline(workload: str, seconds: float) -> dict:
 def run_reference(args, rank: int) -> dict | None:
     if rank != 0:
         return None
+    if describe(args.workload)[0] == "attn":
+        return {"impl": "reference", "unavailable": "the CPU oracle has no attention"}
     from oracle import oracle
     threads = oracle.default_threads()
     lib = oracle.load()

@@ -188,3 +188,147 @@ def step_bytes_formula(spec: dict, batch: int = 1) -> int:
     layer = (roofline.algorithmic_bytes(Q + 2 * KV, H, B) + roofline.algorithmic_bytes(H, H, B)
              + roofline.algorithmic_bytes(2 * I, H, B) + roofline.algorithmic_bytes(H, I, B))
     return spec["layers"] * layer + roofline.algorithmic_bytes(V, H, B)
+
+
+class AttentionStep:
+    """The attention half of a decode step, chained and captured: per layer the
+    fused Q/K/V projection, rotary positions with the cache write, attention of
+    the new token over the paged cache, and the output projection, behind one
+    call that gives the batch's new tokens their pages and slots. The layers'
+    inputs are not chained (as in DecodeStep): each reads its own x.
+
+    ``context``: tokens each request holds already (an int, or one per request).
+    With ``advance`` every step appends a token (lengths and the place in the
+    free list move on in place, so a replayed graph is one step after the
+    other), for up to ``room`` steps; without, every step writes the same token
+    again. ``cache``: "bf16" or "fp8" (E4M3, a scale per key-value head).
+    """
+
+    def __init__(self, spec: dict, context, batch: int = 1, seed: int = 0, device="cuda", cache: str = "bf16",
+                 head_dim: int = 128, page_size: int = 16, advance: bool = False, room: int = 64,
+                 rope_base: float = 500000.0):
+        if not 1 <= batch <= binding.GEMV_MAX_BATCH:
+            raise ValueError("batch must be 1..16")
+        if cache not in ("bf16", "fp8"):
+            raise ValueError("cache must be bf16 or fp8")
+        lens = [context] * batch if isinstance(context, int) else list(context)
+        if len(lens) != batch or min(lens) < 0:
+            raise ValueError("context must be a length, or one per request")
+        self.spec, self.batch, self.cache, self.head_dim, self.page_size = spec, batch, cache, head_dim, page_size
+        self.context, self.advance, self.device = lens, advance, device
+        H, Q, KV = spec["hidden"], spec["q_rows"], spec["kv_rows"]
+        if Q % head_dim or KV % head_dim:
+            raise ValueError("q_rows and kv_rows must be whole heads")
+        self.q_heads, self.kv_heads = Q // head_dim, KV // head_dim
+        self.ldw_h, self.ldw_q = inputs.padded_ldw(H), inputs.padded_ldw(Q)
+        g = torch.Generator(device=device)
+        g.manual_seed(seed)
+
+        # Pages: what the requests hold, then room for the steps, in a shuffled order.
+        have = [-(-n // page_size) for n in lens]
+        self.width = max(-(-(n + room) // page_size) for n in lens)
+        spare = sum(-(-(n + room) // page_size) for n in lens) - sum(have)
+        self.num_pages = sum(have) + spare
+        order = torch.randperm(self.num_pages, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
+        table = torch.full((batch, self.width), -1, dtype=torch.int32)
+        at = 0
+        for r, n in enumerate(have):
+            table[r, :n] = order[at:at + n]
+            at += n
+        i32 = dict(dtype=torch.int32, device=device)
+        self.table = table.to(device)
+        self.free = order[at:].contiguous().to(device)
+        self.free_next = torch.zeros(1, **i32)
+        self.lens = torch.tensor(lens, **i32)
+        self.new_lens = self.lens if advance else torch.empty(batch, **i32)
+        free_next_out = self.free_next if advance else torch.empty(1, **i32)
+        self.ones = torch.ones(batch, **i32)
+        self.slots, self.positions, self.page_start, self.status = (torch.empty(batch, **i32) for _ in range(4))
+        self.token_start = torch.empty(batch + 1, **i32)
+        self.tables = binding.block_tables_args(
+            lens=self.lens, new_tokens=self.ones, requests=batch, page_size=page_size, num_pages=self.num_pages,
+            table=self.table, table_width=self.width, table_stride=self.width, free_pages=self.free,
+            free_cap=self.free.numel(), free_next=self.free_next, max_tokens=batch, slots=self.slots,
+            positions=self.positions, token_start=self.token_start, page_start=self.page_start,
+            new_lens=self.new_lens, status=self.status, free_next_out=free_next_out)
+
+        self.inv_freq = [rope_base ** (-2.0 * i / head_dim) for i in range(head_dim // 2)]
+        self.freqs = binding.rope_freqs(self.inv_freq, device=device)
+        self.workspace = binding.attn_workspace(self.q_heads, self.kv_heads, head_dim, device=device)
+        self.layers = []
+        for l in range(spec["layers"]):
+            self.layers.append(self._layer(l, seed, g))
+        self._graph = None
+
+    def _layer(self, l: int, seed: int, g) -> dict:
+        H, Q, KV = self.spec["hidden"], self.spec["q_rows"], self.spec["kv_rows"]
+        B, D, dev = self.batch, self.head_dim, self.device
+        base = 16 * l
+        d = dict(x=inputs.activations(B, H, seed=seed, index=base + 14, device=dev),
+                 W=[inputs.weight(n, H, self.ldw_h, seed=seed, index=base + j, device=dev)
+                    for j, n in enumerate((Q, KV, KV))],
+                 Wo=inputs.weight(H, Q, self.ldw_q, seed=seed, index=base + 3, device=dev),
+                 y=[torch.empty((B, n), dtype=torch.float32, device=dev) for n in (Q, KV, KV)],
+                 q=torch.empty((B, Q), dtype=torch.bfloat16, device=dev),
+                 out=torch.empty((B, Q), dtype=torch.bfloat16, device=dev),
+                 o=torch.empty((B, H), dtype=torch.float32, device=dev))
+        shape = (self.num_pages, self.page_size, self.kv_heads, D)
+        scales = [None, None]
+        for i, n in enumerate(("k", "v")):
+            d[n] = torch.randn(shape, generator=g, device=dev, dtype=torch.bfloat16)
+            if self.cache == "fp8":
+                d[n] = (d[n] * 32).to(torch.float8_e4m3fn)
+                scales[i] = torch.full((self.kv_heads,), 1.0 / 32, device=dev)
+        d["scales"] = scales
+        d["cache"] = binding.kv_cache(
+            d["k"], d["v"], num_pages=self.num_pages, page_size=self.page_size, kv_heads=self.kv_heads, head_dim=D,
+            page_stride=self.page_size * KV, head_stride=D, slot_stride=KV,
+            kind=binding.GEMV_CACHE_FP8 if self.cache == "fp8" else binding.GEMV_CACHE_BF16,
+            k_scale=scales[0], v_scale=scales[1])
+        d["rope"] = binding.rope_args(
+            q=d["y"][0], k=d["y"][1], v=d["y"][2], q_out=d["q"], positions=self.positions, freqs=self.freqs,
+            tokens=B, q_heads=self.q_heads, kv_heads=self.kv_heads, head_dim=D, rot_dim=D, q_stride=Q, k_stride=KV,
+            v_stride=KV, q_out_stride=Q, slots=self.slots, rows=binding.GEMV_ROWS_F32)
+        d["attn"] = binding.attn_args(
+            q=d["q"], out=d["out"], lens=self.new_lens, requests=B, q_heads=self.q_heads, q_stride=Q, out_stride=Q,
+            table=self.table, table_width=self.width, table_stride=self.width, scale=D ** -0.5,
+            workspace=self.workspace, token_start=self.token_start, rows=B)
+        d["segments"] = [(W, y, W.shape[0], self.ldw_h) for W, y in zip(d["W"], d["y"])]
+        return d
+
+    @property
+    def launches(self) -> int:
+        return 1 + 4 * len(self.layers)
+
+    def run(self, stream=None) -> None:
+        """One step, launch by launch."""
+        H, Q, B = self.spec["hidden"], self.spec["q_rows"], self.batch
+        binding.gemv_block_tables(self.tables, stream)
+        for d in self.layers:
+            binding.gemv_bf16_multi(d["segments"], d["x"], H, B, stream)
+            binding.gemv_rope_append(d["rope"], d["cache"], stream)
+            binding.gemv_attn_decode(d["attn"], d["cache"], stream)
+            binding.gemv_bf16(d["Wo"], d["out"], d["o"], H, Q, B, self.ldw_q, stream)
+
+    def capture(self) -> None:
+        """The step as one CUDA graph. Nothing executes, but a first call on the
+        device must have been made."""
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+            self.run()
+        self._graph = graph
+
+    def launch(self) -> None:
+        """Replay the captured step on the current stream."""
+        self._graph.replay()
+
+    def algorithmic_bytes(self) -> int:
+        """Per step: weights, activations and projections' outputs as in
+        DecodeStep; q, k and v rows read, q and the new slots written; the
+        visible tokens' K and V and q read, the attention's output written."""
+        H, Q, KV, B = self.spec["hidden"], self.spec["q_rows"], self.spec["kv_rows"], self.batch
+        es = 1 if self.cache == "fp8" else 2
+        layer = (roofline.algorithmic_bytes(Q + 2 * KV, H, B) + roofline.algorithmic_bytes(H, Q, B)
+                 + B * (4 * (Q + 2 * KV) + 2 * Q + 2 * KV * es)
+                 + 2 * sum(n + 1 for n in self.context) * KV * es + B * 4 * Q)
+        return len(self.layers) * layer

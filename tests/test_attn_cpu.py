@@ -172,3 +172,11 @@ def test_block_tables_definition():
     assert got == dict(slots=[19, 4, 8, -1, -1], positions=[3, 4, 8, 0, 0], token_start=[0, 2, 2, 3],
                        page_start=[1, 2, 2], new_lens=[5, 0, 9], status=[0, 0, 0], free_next=3,
                        table=[[4, 1, -1], [-1, -1, -1], [6, 7, 2]])
+
+
+def test_attention_workload_is_described():
+    import bench
+    assert bench.describe("attn_step:B16:L4096") == ("attn", None, 4096, 16)
+    assert bench.describe("f8:attn_step:B1:L100") == ("attn", None, 100, 1)
+    with pytest.raises(SystemExit):
+        bench.describe("attn_step:B16")
