@@ -528,7 +528,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     };
     using K = std::true_type;
     using V = std::false_type;
-    if (mine > 0) fetch_query(attn_row(p, r), h);
+    if (mine > 0) {
+        look_ahead();                     // the first pages are on their way,
+        fetch_query(attn_row(p, r), h);   // and the first row's queries
+    }
 #pragma unroll 1
     for (int i = 0; i < E; ++i) {
         if (i & 1) issue(V{});
@@ -1030,17 +1033,21 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // groups' results by the last group. Piece 1 of a row's first CTA, piece 0 of the others; a group's result takes
     // the place of its last piece.
     constexpr int kJoin = 32;
-    __threadfence();
-    __syncthreads();
+    __syncthreads();                      // the CTA's pieces are written; whoever counts it in makes them visible
     // The first and last CTA of the row from before (lanes 0 and 1), of the one after (lanes 2 and 3).
     const Piece cut = lane < 2 ? before : after;
     const int ends = (f0 + cut.at - cut.s + (lane & 1 ? cut.ns - 1 : 0)) / quota;
     const int from0 = __shfl_sync(0xffffffffu, ends, 0), to0 = __shfl_sync(0xffffffffu, ends, 1);
     const int from1 = __shfl_sync(0xffffffffu, ends, 2), to1 = __shfl_sync(0xffffffffu, ends, 3);
     // One more arrival at a counter; whether it is the last of `all`, with the counter zero again for the next call.
+    // By one thread behind a barrier of the CTA, before and after: its fences stand for all threads.
     auto arrive = [&](uint32_t* ticket, int all) {
+        __threadfence();
         const bool last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(all - 1);
-        if (last) *ticket = 0u;
+        if (last) {
+            *ticket = 0u;
+            __threadfence();
+        }
         return last;
     };
     uint32_t* const of_rows = p.ticket + qt;
@@ -1085,19 +1092,25 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 }
             }
 #pragma unroll
-            for (int b = 0; b < B; ++b)
+            for (int u = 0; u < UW; ++u) {
+                float next = top[u];
 #pragma unroll
-                for (int u = 0; u < UW; ++u)
-                    if (ml[b][u].x != kNegInf) {
-                        const float next = fmaxf(top[u], ml[b][u].x);
-                        const float e = exp2_ftz(top[u] - next), f = exp2_ftz(ml[b][u].x - next);
-                        sum[u] = sum[u] * e + ml[b][u].y * f;
-                        o[u].x = o[u].x * e + v[b][u].x * f;
-                        o[u].y = o[u].y * e + v[b][u].y * f;
-                        o[u].z = o[u].z * e + v[b][u].z * f;
-                        o[u].w = o[u].w * e + v[b][u].w * f;
-                        top[u] = next;
+                for (int b = 0; b < B; ++b) next = fmaxf(next, ml[b][u].x);
+                const float base = next == kNegInf ? 0.f : next, e = exp2_ftz(top[u] - base);
+                sum[u] *= e;
+                o[u] = make_float4(o[u].x * e, o[u].y * e, o[u].z * e, o[u].w * e);
+                top[u] = next;
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    if (b0 + b < count) {
+                        const float f = exp2_ftz(ml[b][u].x - base);
+                        sum[u] += ml[b][u].y * f;
+                        o[u].x += v[b][u].x * f;
+                        o[u].y += v[b][u].y * f;
+                        o[u].z += v[b][u].z * f;
+                        o[u].w += v[b][u].w * f;
                     }
+            }
         }
     };
     auto store_row = [&](int r, int hk, float scale) {
@@ -1110,7 +1123,6 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         if (s_last[k] != kLast) continue;
-        __threadfence();
         const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1;
         join(std::integral_constant<int, 16 / UW>{}, from, to - from + 1, [&](int b) { return from + b; });
         store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
@@ -1128,7 +1140,6 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         if (tid == 0) s_last[k] = arrive(p.ticket + kAttnTickets / 2 + end * p.qtiles + qt, end - begin + 1);
         __syncthreads();
         if (!s_last[k]) continue;
-        __threadfence();
         using Few = std::integral_constant<int, UW == 4 ? 2 : 8 / UW>;
         join(Few{}, from, end - begin + 1, [&](int b) { return begin + b; });
         __syncthreads();                                             // every thread has read the group's pieces
@@ -1140,12 +1151,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             *reinterpret_cast<float4*>(p.part + at * DT + d) = o[u];
             if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top[u], sum[u]);
         }
-        __threadfence();
         __syncthreads();
         if (tid == 0) s_last[k] = arrive(of_rows + from * p.qtiles, groups);
         __syncthreads();
         if (!s_last[k]) continue;
-        __threadfence();
         join(Few{}, -1, groups, [&](int b) { return min(from + (b + 1) * g - 1, to); });
         store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
     }
