@@ -295,6 +295,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.kv_heads = c->kv_heads;
     p.group = group;
     p.qtiles = l.qtiles;
+    p.team_shift = l.team_shift;
     p.head_dim = c->head_dim;
     p.page_size = c->page_size;
     p.table_width = a->table_width;

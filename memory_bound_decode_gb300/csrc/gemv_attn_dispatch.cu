@@ -21,7 +21,8 @@ GEMV_ATTN_DECL(fp8_256)
 // many blocks of 8 query heads as the group needs, up to what the output
 // accumulators leave room for (32 heads; 16 where a head has over 128
 // columns). A larger group is cut into tiles, one per CTA of a set of CTAs
-// that read the same tokens at the same time.
+// that read the same tokens at the same time. CTAs also form teams of 2, 4 or
+// 8, as far as both the KV heads and the CTAs divide, a head of a block each.
 int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, AttnLaunch* l) {
     const int group = q_heads / kv_heads;
     l->fp8 = fp8;
@@ -31,6 +32,8 @@ int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, At
     l->nb = blocks <= 1 ? 1 : blocks <= 2 || most == 2 ? 2 : 4;
     l->qtiles = (blocks + l->nb - 1) / l->nb;
     l->grid = std::max(1, sm_count / l->qtiles) * l->qtiles;
+    l->team_shift = 0;
+    while (l->team_shift < 3 && ((kv_heads | l->grid / l->qtiles) >> l->team_shift & 1) == 0) ++l->team_shift;
     if (l->grid > kAttnTickets / 2) return GEMV_ERR_UNSUPPORTED;
     const int64_t heads = static_cast<int64_t>(l->grid) * (2 + kAttnWarps) * l->nb * 8;   // pieces of CTAs and warps
     l->workspace_bytes = kAttnTickets * 4 + heads * (2 + l->dt) * 4;

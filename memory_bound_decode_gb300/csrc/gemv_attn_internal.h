@@ -57,7 +57,7 @@ struct AttnParams {
     int64_t q_stride, out_stride, table_stride;
     int64_t page_stride, head_stride, slot_stride;   // bytes
     int64_t rows;               // rows of q and out
-    int32_t requests, q_heads, kv_heads, group, qtiles;
+    int32_t requests, q_heads, kv_heads, group, qtiles, team_shift;
     int32_t head_dim, page_size, table_width, num_pages, window, max_len;
     int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
     int32_t tma;                // 1: tensor copies of box_rows slots
@@ -71,7 +71,7 @@ struct AttnLaunch {
     int fp8;
     int warps;
     int slice;         // tokens a warp takes at a time
-    int qtiles, grid;
+    int qtiles, team_shift, grid;
     int64_t workspace_bytes;
 };
 

@@ -239,8 +239,15 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int qt = blockIdx.x % p.qtiles;
-    const int cta = blockIdx.x / p.qtiles;
-    const int ctas = gridDim.x / p.qtiles;
+    // CTAs work in teams of 2, 4 or 8 where the KV heads divide into such blocks: the list is one of head blocks, and
+    // each CTA of a team takes its own head of the block. They read neighbouring memory at the same time, and the HBM
+    // gives more for it (FP8, 32 x 16,384 tokens: 220 -> 167 us; BF16, 64 x 32,768: 927 -> 884).
+    const int blocks = p.kv_heads >> p.team_shift;
+    const int cta = blockIdx.x / p.qtiles >> p.team_shift, ctas = gridDim.x / p.qtiles >> p.team_shift;
+    const int member = blockIdx.x / p.qtiles & ((1 << p.team_shift) - 1);
+    auto head_of = [&](int block) { return (block << p.team_shift) + member; };
+    // The place in the grid of this team's CTA c (of this one's head).
+    auto place_of = [&](int c) { return ((c << p.team_shift) + member) * p.qtiles + qt; };
     const int head0 = qt * H;                                        // first query head of the group
     const int nh = min(H, p.group - head0);                          // query heads of this tile
     unsigned char* const ring_p = smem + w * kAttnRing;
@@ -309,18 +316,33 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     }
 
     // ---- the CTA's range f0 .. f0 + cnt of the list, this warp's part of it, and the requests the parts begin in ----
-    total *= p.kv_heads;                                             // below 2^31: checked by the host
+    const bool alike = p.requests <= T && static_cast<int64_t>(longest) * p.requests == total;   // (one request, say)
+    total *= blocks;                                                 // below 2^31: checked by the host
     // At least a slice per warp. Rows of up to two per warp are better not cut between CTAs, and of up to four if
     // that leaves work for a quarter of the CTAs: the slices of a warp come 1.3 us after each other, a join across
     // CTAs takes 4 (8 x 1,000 tokens: 12.6 us against 16.0; 1 x 1,000: 11.9 against 10.3).
     const bool uncut = longest <= 2 * W || (longest <= 4 * W && total / longest * 4 >= ctas);
-    const int quota = max((total + ctas - 1) / ctas, max(W, uncut ? longest : 0));
-    const int f0 = cta * quota;                                      // below total + grid * quota
+    int quota = max((total + ctas - 1) / ctas, max(W, uncut ? longest : 0));
+    // Rows of one length go to CTAs of their own where that adds no more than a slice per warp (a CTA between two rows
+    // may be the last of both and join them one after the other: 1 x 8,000 tokens 17.7 us, so 15.0), or where a warp
+    // has up to 16 slices (a join less: 13 x 2,000 tokens 26.0 -> 22.6 us, 16 x 4,000 48.0 -> 44.4; but 10 x 4,000
+    // 34.2 -> 35.8).
+    int per_row = 0;                                                 // CTAs of a row, or 0
+    if (alike && !uncut && total > 0 && total / longest <= ctas) {
+        const int most = ctas / (total / longest), q = max(W, (longest + most - 1) / most);
+        if (q <= max(quota + W, 16 * W)) {
+            quota = q;
+            per_row = (longest + q - 1) / q;
+            if (cta >= total / longest * per_row) return;
+        }
+    }
+    const int in_row = per_row ? cta % per_row * quota : 0;
+    const int f0 = per_row ? cta / per_row * longest + in_row : cta * quota;   // below total + grid * quota
     if (f0 >= total) return;
-    const int cnt = min(quota, total - f0);
+    const int cnt = min(quota, per_row ? longest - in_row : total - f0);
     const int part = (cnt + W - 1) / W;
     auto claim = [&](int r, int n, int end) {                        // `end`: slices up to request r, a head
-        const int lo = (end - n) * p.kv_heads - f0, hi = end * p.kv_heads - f0;
+        const int lo = (end - n) * blocks - f0, hi = end * blocks - f0;
 #pragma unroll 1
         for (int i = 0; i < W && n > 0; ++i)
             if (lo <= i * part && i * part < hi) {
@@ -331,7 +353,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     claim(tid, n_first, incl);
     int len0 = 0;
 #pragma unroll 1
-    for (int base = T; base < p.requests && carry * p.kv_heads < f0 + cnt; base += T) {   // the same for all threads
+    for (int base = T; base < p.requests && carry * blocks < f0 + cnt; base += T) {   // the same for all threads
         const int len = base + tid < p.requests ? attn_len(p, base + tid) : -1;
         const int n = attn_slices<TS>(p, len);
         incl = n;
@@ -366,7 +388,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     }
 
     // ---- queries of a row, as they come, into q_raw ----
-    auto fetch_query = [&](int64_t row, int hk) {
+    auto fetch_query = [&](int64_t row, int block) {
+        const int hk = head_of(block);
         const unsigned char* src = reinterpret_cast<const unsigned char*>(
             p.q + row * p.q_stride + (static_cast<int64_t>(hk) * p.group + head0) * p.head_dim);
         const int per = p.head_dim / 4;                              // 8-byte pieces of a head
@@ -429,7 +452,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll 1
             while (us >= ns) {
                 us -= ns;
-                if (++uh == p.kv_heads) {
+                if (++uh == blocks) {
                     uh = 0;
 #pragma unroll 1
                     do {
@@ -491,7 +514,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 const int of = (issued & (batch - 1)) * per_slice, i = TMA ? lane / LINES : lane & (TS - 1);
                 const int page = __shfl_sync(0xffffffffu, now.page, (of + i) & 31);
                 const int place = __shfl_sync(0xffffffffu, now.in, (of + i) & 31);
-                const int head = __shfl_sync(0xffffffffu, now.h, of);
+                const int head = head_of(__shfl_sync(0xffffffffu, now.h, of));
                 last_valid = __shfl_sync(0xffffffffu, now.valid, of);
                 const bool has = i < per_slice && place >= 0;
                 const bool in = has && page >= 0 && page < p.num_pages;
@@ -643,7 +666,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 
         // The row after this one.
         int next_r = r, next_h = h;
-        if (seg < left && ++next_h == p.kv_heads) {
+        if (seg < left && ++next_h == blocks) {
             next_h = 0;
 #pragma unroll 1
             do ++next_r;
@@ -869,7 +892,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             }
         const bool whole = s == 0 && seg == ns, final = seg == left;
         if (whole) {
-            const int64_t head_at = static_cast<int64_t>(h) * p.group + head0;
+            const int64_t head_at = static_cast<int64_t>(head_of(h)) * p.group + head0;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 float inv[2];
@@ -934,8 +957,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     __syncthreads();
 
     // ---- the warps' pieces, joined row by row ----
-    auto store = [&](int r, int hk, int hd, int d, float4 o, float top, float sum, float scale) {
-        const int64_t row = attn_row(p, r), head = static_cast<int64_t>(hk) * p.group + head0 + hd;
+    auto store = [&](int r, int block, int hd, int d, float4 o, float top, float sum, float scale) {
+        const int64_t row = attn_row(p, r), head = static_cast<int64_t>(head_of(block)) * p.group + head0 + hd;
         const float inv = sum == 0.f ? 0.f : scale / sum;
         *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * p.head_dim + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
@@ -1036,7 +1059,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     __syncthreads();                      // the CTA's pieces are written; whoever counts it in makes them visible
     // The first and last CTA of the row from before (lanes 0 and 1), of the one after (lanes 2 and 3).
     const Piece cut = lane < 2 ? before : after;
-    const int ends = (f0 + cut.at - cut.s + (lane & 1 ? cut.ns - 1 : 0)) / quota;
+    const int row0 = f0 + cut.at - cut.s;                            // where it starts in the list
+    const int ends = per_row ? row0 / longest * per_row + (lane & 1 ? per_row - 1 : 0)
+                             : (row0 + (lane & 1 ? cut.ns - 1 : 0)) / quota;
     const int from0 = __shfl_sync(0xffffffffu, ends, 0), to0 = __shfl_sync(0xffffffffu, ends, 1);
     const int from1 = __shfl_sync(0xffffffffu, ends, 2), to1 = __shfl_sync(0xffffffffu, ends, 3);
     // One more arrival at a counter; whether it is the last of `all`, with the counter zero again for the next call.
@@ -1050,23 +1075,28 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         }
         return last;
     };
-    uint32_t* const of_rows = p.ticket + qt;
     enum { kWait, kLast, kGroups };
     if (lane == 0 && w < 2) {
         int state = kWait;
         if (w == 0 ? before.valid : after.valid) {
             const int from = w == 0 ? from0 : from1, n = (w == 0 ? to0 : to1) - from + 1;
-            state = n > kJoin ? kGroups : arrive(of_rows + from * p.qtiles, n) ? kLast : kWait;
+            state = n > kJoin ? kGroups : arrive(p.ticket + place_of(from), n) ? kLast : kWait;
         }
         s_last[w] = state;
     }
     __syncthreads();
 
-    // Joins `count` pieces, those of cta_of(0), cta_of(1), ..: B at a time, all of whose loads are in flight together.
+    // Joins the pieces of CTAs c0, c0 + step, .. up to `end` (the last one always `end`). Narrow tiles leave threads
+    // over: `parts` threads share an item then, each with every parts-th piece, and meet in the ring. B at a time,
+    // all of whose loads are in flight together.
+    constexpr int B = UW == 1 ? 5 : UW == 2 ? 8 : 4;
+    const int parts = UW > 1 || 2 * items > T ? 1 : 4 * items > T ? 2 : 4;
+    const int mine_of = UW > 1 || tid < items ? 0 : tid / items;     // >= parts: idle
+    const int item = tid - mine_of * items;
     float top[UW], sum[UW];
     float4 o[UW];
-    auto join = [&](auto batch, int from, int count, auto cta_of) {
-        constexpr int B = decltype(batch)::value;
+    auto join = [&](int from, int c0, int step, int end) {
+        const int count = (end - c0 + step - 1) / step + 1;
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
             top[u] = kNegInf;
@@ -1074,20 +1104,21 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll 1
-        for (int b0 = 0; b0 < count; b0 += B) {
+        for (int b0 = mine_of; b0 < count && mine_of < parts; b0 += B * parts) {
             float2 ml[B][UW];
             float4 v[B][UW];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const int c = cta_of(b0 + b);
-                const int64_t at = ((static_cast<int64_t>(c) * p.qtiles + qt) * 2 + (c == from ? 1 : 0)) * H;
+                const int at_b = b0 + b * parts, c = min(c0 + at_b * step, end);
+                const int at = (place_of(c) * 2 + (c == from ? 1 : 0)) * H;   // heads of pieces: below 2^31
 #pragma unroll
                 for (int u = 0; u < UW; ++u) {
-                    const int x = u * T + tid, hd = x / d4s, d = (x - hd * d4s) * 4;
+                    const int x = u * T + item, hd = x / d4s, d = (x - hd * d4s) * 4;
                     ml[b][u] = make_float2(kNegInf, 0.f);
-                    if (b0 + b < count && x < items) {
-                        ml[b][u] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (at + hd) * 2));
-                        v[b][u] = __ldcg(reinterpret_cast<const float4*>(p.part + (at + hd) * DT + d));
+                    v[b][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (at_b < count && x < items) {
+                        ml[b][u] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at + hd);
+                        v[b][u] = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(at + hd) * DT + d));
                     }
                 }
             }
@@ -1101,15 +1132,37 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 o[u] = make_float4(o[u].x * e, o[u].y * e, o[u].z * e, o[u].w * e);
                 top[u] = next;
 #pragma unroll
-                for (int b = 0; b < B; ++b)
-                    if (b0 + b < count) {
-                        const float f = exp2_ftz(ml[b][u].x - base);
-                        sum[u] += ml[b][u].y * f;
-                        o[u].x += v[b][u].x * f;
-                        o[u].y += v[b][u].y * f;
-                        o[u].z += v[b][u].z * f;
-                        o[u].w += v[b][u].w * f;
-                    }
+                for (int b = 0; b < B; ++b) {
+                    const float f = exp2_ftz(ml[b][u].x - base);
+                    sum[u] += ml[b][u].y * f;
+                    o[u].x += v[b][u].x * f;
+                    o[u].y += v[b][u].y * f;
+                    o[u].z += v[b][u].z * f;
+                    o[u].w += v[b][u].w * f;
+                }
+            }
+        }
+        if constexpr (UW == 1) {
+            if (parts == 1) return;
+            float4* const s_o = reinterpret_cast<float4*>(smem);
+            float2* const s_x = reinterpret_cast<float2*>(smem + T * 16);
+            __syncthreads();                                         // the ring has been read
+            s_o[tid] = o[0];
+            s_x[tid] = make_float2(top[0], sum[0]);
+            __syncthreads();
+            if (mine_of != 0) return;
+#pragma unroll 1
+            for (int k = 1; k < parts; ++k) {
+                const float2 ml = s_x[k * items + tid];
+                const float4 v = s_o[k * items + tid];
+                const float next = fmaxf(top[0], ml.x), base = next == kNegInf ? 0.f : next;
+                const float e = exp2_ftz(top[0] - base), f = exp2_ftz(ml.x - base);
+                top[0] = next;
+                sum[0] = sum[0] * e + ml.y * f;
+                o[0].x = o[0].x * e + v.x * f;
+                o[0].y = o[0].y * e + v.y * f;
+                o[0].z = o[0].z * e + v.z * f;
+                o[0].w = o[0].w * e + v.w * f;
             }
         }
     };
@@ -1124,7 +1177,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     for (int k = 0; k < 2; ++k) {
         if (s_last[k] != kLast) continue;
         const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1;
-        join(std::integral_constant<int, 16 / UW>{}, from, to - from + 1, [&](int b) { return from + b; });
+        join(from, from, 1, to);
         store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
     }
     if (s_last[0] != kGroups && s_last[1] != kGroups) return;
@@ -1137,25 +1190,24 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         const int begin = from + (cta - from) / g * g, end = min(begin + g - 1, to);
         // Groups are counted at their last CTA, which no other row's group ends at.
         __syncthreads();                                             // s_last has been read
-        if (tid == 0) s_last[k] = arrive(p.ticket + kAttnTickets / 2 + end * p.qtiles + qt, end - begin + 1);
+        if (tid == 0) s_last[k] = arrive(p.ticket + kAttnTickets / 2 + place_of(end), end - begin + 1);
         __syncthreads();
         if (!s_last[k]) continue;
-        using Few = std::integral_constant<int, UW == 4 ? 2 : 8 / UW>;
-        join(Few{}, from, end - begin + 1, [&](int b) { return begin + b; });
+        join(from, begin, 1, end);
         __syncthreads();                                             // every thread has read the group's pieces
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
             const int x = u * T + tid, hd = x / d4s, d = (x - hd * d4s) * 4;
             if (x >= items) break;
-            const int64_t at = (static_cast<int64_t>(end) * p.qtiles + qt) * 2 * H + hd;
+            const int64_t at = static_cast<int64_t>(place_of(end)) * 2 * H + hd;
             *reinterpret_cast<float4*>(p.part + at * DT + d) = o[u];
             if (d == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(top[u], sum[u]);
         }
         __syncthreads();
-        if (tid == 0) s_last[k] = arrive(of_rows + from * p.qtiles, groups);
+        if (tid == 0) s_last[k] = arrive(p.ticket + place_of(from), groups);
         __syncthreads();
         if (!s_last[k]) continue;
-        join(Few{}, -1, groups, [&](int b) { return min(from + (b + 1) * g - 1, to); });
+        join(-1, from + g - 1, g, to);
         store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
     }
 }
