@@ -168,8 +168,8 @@ static __device__ __noinline__ int attn_len(const AttnParams& p, int r) {
     }
     return attn_cut(p, len);
 }
-__device__ __forceinline__ int64_t attn_row(const AttnParams& p, int r) {
-    return p.token_start ? static_cast<int64_t>(p.token_start[r + 1]) - 1 : r;
+__device__ __forceinline__ int attn_row(const AttnParams& p, int r) {
+    return p.token_start ? p.token_start[r + 1] - 1 : r;
 }
 __device__ __forceinline__ int attn_begin(const AttnParams& p, int len) {
     return p.window > 0 && len > p.window ? len - p.window : 0;
@@ -222,6 +222,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // A piece of a row: slices s .. s + seg - 1 of ns, the first of them slice `at` of the CTA's range.
     struct Piece {
         int valid, r, h, s, seg, ns, at;
+        int row;                          // of q and out
         float v_scale;
     };
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -308,11 +309,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // Requests without a visible token: zeros (nothing to average), from the CTA whose turn it is.
     for (int r = blockIdx.x; r < p.requests; r += gridDim.x) {
         if ((r < T ? s_len[r] : attn_len(p, r)) != 0) continue;
-        const int64_t row = attn_row(p, r);
-        uint2* o = reinterpret_cast<uint2*>(p.out + row * p.out_stride);
+        const int row = attn_row(p, r);
+        uint2* o = reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * p.out_stride);
         for (int i = tid; i < p.q_heads * p.head_dim / 4; i += T) o[i] = make_uint2(0, 0);
         if (p.lse)
-            for (int i = tid; i < p.q_heads; i += T) p.lse[row * p.q_heads + i] = kNegInf;
+            for (int i = tid; i < p.q_heads; i += T) p.lse[static_cast<int64_t>(row) * p.q_heads + i] = kNegInf;
     }
 
     // ---- the CTA's range f0 .. f0 + cnt of the list, this warp's part of it, and the requests the parts begin in ----
@@ -388,10 +389,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     }
 
     // ---- queries of a row, as they come, into q_raw ----
-    auto fetch_query = [&](int64_t row, int block) {
+    auto fetch_query = [&](int row, int block) {
         const int hk = head_of(block);
         const unsigned char* src = reinterpret_cast<const unsigned char*>(
-            p.q + row * p.q_stride + (static_cast<int64_t>(hk) * p.group + head0) * p.head_dim);
+            p.q + static_cast<int64_t>(row) * p.q_stride + (static_cast<int64_t>(hk) * p.group + head0) * p.head_dim);
         const int per = p.head_dim / 4;                              // 8-byte pieces of a head
         const uint32_t to = smem_addr(q_raw);
 #pragma unroll 1
@@ -661,7 +662,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         const int ns = attn_slices<TS>(p, len);
         const int seg = min(ns - s, left);
         if (seg <= 0) break;                                         // only if lens changed under the call
-        const int64_t row = attn_row(p, r);
+        const int row = attn_row(p, r);
         place_query();
 
         // The row after this one.
@@ -901,11 +902,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     const int hd = nb * 8 + 2 * t + j;
                     inv[j] = l[nb][j] == 0.f ? 0.f : v_scale / l[nb][j];
                     if (p.lse && g == 0 && hd < nh)
-                        p.lse[row * p.q_heads + head_at + hd] =
+                        p.lse[static_cast<int64_t>(row) * p.q_heads + head_at + hd] =
                             m[nb][j] == kNegInf ? kNegInf : (m[nb][j] + log2f(l[nb][j])) * kLn2;
                 }
                 // Transposed again, lane (g, t) holds columns 2t, 2t + 1 of the tile's rows for head g.
-                uint16_t* const o = p.out + row * p.out_stride + (head_at + nb * 8 + g) * p.head_dim;
+                uint16_t* const o = p.out + static_cast<int64_t>(row) * p.out_stride + (head_at + nb * 8 + g) * p.head_dim;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const uint32_t a = transpose8x8(pack_bf16(acc[ks][nb][0] * inv[0], acc[ks][nb][1] * inv[1]));
@@ -941,7 +942,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                         }
                     }
                 }
-            if (lane == 0) s_piece[2 * w + (final ? 1 : 0)] = {1, r, h, s, seg, ns, at, v_scale};
+            if (lane == 0) s_piece[2 * w + (final ? 1 : 0)] = {1, r, h, s, seg, ns, at, row, v_scale};
         }
 
         left -= seg;
@@ -957,16 +958,16 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     __syncthreads();
 
     // ---- the warps' pieces, joined row by row ----
-    auto store = [&](int r, int block, int hd, int d, float4 o, float top, float sum, float scale) {
-        const int64_t row = attn_row(p, r), head = static_cast<int64_t>(head_of(block)) * p.group + head0 + hd;
+    auto store = [&](int row, int block, int hd, int d, float4 o, float top, float sum, float scale) {
+        const int64_t head = static_cast<int64_t>(head_of(block)) * p.group + head0 + hd;
         const float inv = sum == 0.f ? 0.f : scale / sum;
-        *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * p.head_dim + d) =
+        *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * p.out_stride + head * p.head_dim + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (p.lse && d == 0) p.lse[row * p.q_heads + head] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
+        if (p.lse && d == 0) p.lse[static_cast<int64_t>(row) * p.q_heads + head] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
     };
     const int d4s = p.head_dim / 4, items = nh * d4s;
     // Every warp finds the rows among the pieces by itself: lane i holds piece i.
-    Piece own = {0, -1, -1, 0, 0, 0, 0, 1.f};
+    Piece own = {0, -1, -1, 0, 0, 0, 0, 0, 1.f};
     if (lane < 2 * W) own = s_piece[lane];
     const uint32_t pieces = __ballot_sync(0xffffffffu, own.valid != 0);
     uint32_t starts;                      // the first piece of each row
@@ -985,6 +986,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         a.seg = __shfl_sync(0xffffffffu, own.seg, i);
         a.ns = __shfl_sync(0xffffffffu, own.ns, i);
         a.at = __shfl_sync(0xffffffffu, own.at, i);
+        a.row = __shfl_sync(0xffffffffu, own.row, i);
         a.v_scale = __shfl_sync(0xffffffffu, own.v_scale, i);
         return a;
     };
@@ -1041,7 +1043,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     o.w += v.w * e;
                 }
             if (whole) {
-                store(a.r, a.h, hd, d, o, top, sum, a.v_scale);
+                store(a.row, a.h, hd, d, o, top, sum, a.v_scale);
             } else {
                 *reinterpret_cast<float4*>(p.part + (piece * H + hd) * DT + d) = o;
                 if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (piece * H + hd) * 2) = make_float2(top, sum);
@@ -1166,11 +1168,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             }
         }
     };
-    auto store_row = [&](int r, int hk, float scale) {
+    auto store_row = [&](const Piece& a) {
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
             const int x = u * T + tid, hd = x / d4s;
-            if (x < items) store(r, hk, hd, (x - hd * d4s) * 4, o[u], top[u], sum[u], scale);
+            if (x < items) store(a.row, a.h, hd, (x - hd * d4s) * 4, o[u], top[u], sum[u], a.v_scale);
         }
     };
 #pragma unroll 1
@@ -1178,7 +1180,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         if (s_last[k] != kLast) continue;
         const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1;
         join(from, from, 1, to);
-        store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
+        store_row(k == 0 ? before : after);
     }
     if (s_last[0] != kGroups && s_last[1] != kGroups) return;
     const bool big[2] = {s_last[0] == kGroups, s_last[1] == kGroups};
@@ -1208,7 +1210,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         __syncthreads();
         if (!s_last[k]) continue;
         join(-1, from + g - 1, g, to);
-        store_row(k == 0 ? before.r : after.r, k == 0 ? before.h : after.h, k == 0 ? before.v_scale : after.v_scale);
+        store_row(k == 0 ? before : after);
     }
 }
 
