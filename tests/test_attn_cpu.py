@@ -180,3 +180,13 @@ def test_attention_workload_is_described():
     assert bench.describe("f8:attn_step:B1:L100") == ("attn", None, 100, 1)
     with pytest.raises(SystemExit):
         bench.describe("attn_step:B16")
+
+
+@pytest.mark.parametrize("over", [
+    dict(requests=1024, table_width=1 << 20, table_stride=1 << 20),      # 1024 * 2 * (2^20 + 2) slices of 16 tokens
+    dict(requests=(1 << 31) - 1),                                        # 2 * (4 + 2) each
+])
+def test_more_slices_than_the_list_holds(over):
+    with pytest.raises(binding.GemvError) as e:
+        binding.gemv_attn_decode(attn(**over), cache())
+    assert e.value.status == UNSUPPORTED

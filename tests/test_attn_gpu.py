@@ -254,3 +254,27 @@ def test_no_requests():
     torch.cuda.synchronize()
     mark = float(torch.tensor(-777.0).bfloat16())
     assert (a.guard.float() == mark).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("heads", [2, 4, 6, 8, 12, 32])
+def test_heads_in_teams(kind, heads):
+    """KV heads that divide into blocks of 2, 4 or 8 (and not): rows in one piece, cut in two, cut in many."""
+    run([5000, 0, 3, 900, 2047, 64, 1, 6500], 4 * heads, heads, 64, 16, kind, "head")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("heads, n, requests", [
+    (8, 700, 1), (8, 1000, 1), (8, 2000, 1), (8, 9001, 1),      # one request: 1, 4, 8 and more CTAs a row
+    (1, 30000, 1), (2, 30000, 1),                               # rows joined in two levels
+    (8, 1000, 8), (8, 2001, 8), (8, 1999, 13), (4, 515, 38),    # a row per CTA, rows in two, no room for all rows
+    (8, 600, 20), (1, 33, 256), (1, 33, 257),                   # more rows than CTAs; the last one counted, the first not
+])
+def test_rows_of_one_length(kind, heads, n, requests):
+    run([n] * requests, 4 * heads, heads, 64, 32, kind, "token")
+
+
+def test_rows_of_one_length_in_groups_of_sixteen_and_wide_heads():
+    run([2500] * 3, 32, 2, 256, 24, "bf16", "head")
+    run([2500] * 3, 64, 4, 128, 16, "bf16", "token")
+    run([2500] * 3, 66, 2, 128, 16, "fp8", "token")             # 33 heads a group: two tiles of them, teams of 2
