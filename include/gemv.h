@@ -707,6 +707,9 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  *           first use (every call leaves it fit for the next, of any shape that
  *           needs no more bytes). Calls that may run at the same time need a
  *           workspace each, replayed graphs among them.
+ * What lens, token_start and table hold must not change while a call runs:
+ * its results are then undefined, and so are later ones with its workspace
+ * until that is zeroed again.
  * Products of BF16 (FP8: codes widened exactly to FP16, and q scaled into FP16
  * by a power of two per head) are summed in FP32, the softmax is kept in FP32;
  * the probabilities meet V as two BF16 parts (FP8: as FP16). requests = 0 is
