@@ -283,7 +283,13 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     pdl_wait_prerequisites();
 
     // ---- the sum of the slices, and (in the first chunk of requests) their running sums ----
-    const int len_first = tid >= p.requests ? -1 : p.token_start ? attn_len(p, tid) : attn_cut(p, p.lens[tid]);
+    // Up to 32 requests each warp sums up for itself, with its copy of the lengths and no barrier (0.5 us less of
+    // every call; 1 x 1,000 tokens 10.7 -> 10.2).
+    const bool few = p.requests <= 32;
+    const int copy = few ? w * 32 : 0, first_of = tid - copy;        // this thread's request of the first chunk
+    const int len_first = first_of >= p.requests ? -1
+                          : p.token_start        ? attn_len(p, first_of)
+                                                 : attn_cut(p, p.lens[first_of]);
     const int n_first = attn_slices<TS>(p, len_first);
     s_len[tid] = len_first;
     int incl = n_first;
@@ -293,15 +299,20 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         if (lane >= o) incl += up;
     }
     int longest = __reduce_max_sync(0xffffffffu, n_first);
-    if (lane == 31) s_scan[w] = make_int2(incl, longest);
-    __syncthreads();
     int carry = 0;
+    if (few) {
+        carry = __shfl_sync(0xffffffffu, incl, 31);
+        __syncwarp();                                                // s_len is written
+    } else {
+        if (lane == 31) s_scan[w] = make_int2(incl, longest);
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const int2 of = s_scan[i];
-        if (i < w) incl += of.x;
-        carry += of.x;
-        longest = max(longest, of.y);
+        for (int i = 0; i < W; ++i) {
+            const int2 of = s_scan[i];
+            if (i < w) incl += of.x;
+            carry += of.x;
+            longest = max(longest, of.y);
+        }
     }
     int total = carry;
     if (p.requests > T) {
@@ -318,7 +329,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 
     // Requests without a visible token: zeros (nothing to average), from the CTA whose turn it is.
     for (int r = blockIdx.x; r < p.requests; r += gridDim.x) {
-        if ((r < T ? s_len[r] : attn_len(p, r)) != 0) continue;
+        if ((r < T ? s_len[copy + r] : attn_len(p, r)) != 0) continue;
         const int row = attn_row(p, r);
         uint2* o = reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * p.out_stride);
         for (int i = tid; i < p.q_heads * p.head_dim / 4; i += T) o[i] = make_uint2(0, 0);
@@ -361,41 +372,49 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 s_off[i] = i * part - lo;
             }
     };
-    claim(tid, n_first, incl);
-    int len0 = 0;
+    int len0 = 0, r, off_r;
+    if (few) {
+        const int lo = (incl - n_first) * blocks - f0, hi = incl * blocks - f0, x = w * part;
+        const uint32_t mine = __ballot_sync(0xffffffffu, n_first > 0 && lo <= x && x < hi && x < cnt);
+        r = mine ? __ffs(mine) - 1 : -1;
+        off_r = x - __shfl_sync(0xffffffffu, lo, max(r, 0));
+    } else {
+        claim(tid, n_first, incl);
 #pragma unroll 1
-    for (int base = T; base < p.requests && carry * blocks < f0 + cnt; base += T) {   // the same for all threads
-        const int len = base + tid < p.requests ? attn_len(p, base + tid) : -1;
-        const int n = attn_slices<TS>(p, len);
-        incl = n;
+        for (int base = T; base < p.requests && carry * blocks < f0 + cnt; base += T) {   // the same for all threads
+            const int len = base + tid < p.requests ? attn_len(p, base + tid) : -1;
+            const int n = attn_slices<TS>(p, len);
+            incl = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            __syncthreads();                                             // s_scan and s_len have been read
+            if (lane == 31) s_scan[w].x = incl;
+            s_len[tid] = len;
+            len0 = base;
+            __syncthreads();
+            int before = carry;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                if (i < w) before += s_scan[i].x;
+                carry += s_scan[i].x;
+            }
+            claim(base + tid, n, before + incl);
         }
-        __syncthreads();                                             // s_scan and s_len have been read
-        if (lane == 31) s_scan[w].x = incl;
-        s_len[tid] = len;
-        len0 = base;
         __syncthreads();
-        int before = carry;
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            if (i < w) before += s_scan[i].x;
-            carry += s_scan[i].x;
-        }
-        claim(base + tid, n, before + incl);
+        r = s_req[w];
+        off_r = s_off[w];
     }
-    __syncthreads();
-    auto len_of = [&](int r) { return r >= len0 && r - len0 < T ? s_len[r - len0] : attn_len(p, r); };
+    auto len_of = [&](int r) { return r >= len0 && r - len0 < T ? s_len[copy + r - len0] : attn_len(p, r); };
     int left = max(0, min(part, cnt - w * part));                    // slices of this warp
-    int r = s_req[w];
     if (r < 0) left = 0;                                             // no part (or lens changed under the call)
     int h = 0, s = 0;
     if (left > 0) {
         const int ns0 = max(1, attn_slices<TS>(p, len_of(r)));
-        h = s_off[w] / ns0;
-        s = s_off[w] - h * ns0;
+        h = off_r / ns0;
+        s = off_r - h * ns0;
     }
 
     // ---- queries of a row, as they come, into q_raw ----
