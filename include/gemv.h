@@ -712,7 +712,8 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * until that is zeroed again.
  * Products of BF16 (FP8: codes widened exactly to FP16, and q scaled into FP16
  * by a power of two per head) are summed in FP32, the softmax is kept in FP32;
- * the probabilities meet V as two BF16 parts (FP8: as FP16). requests = 0 is
+ * the probabilities meet V as two BF16 parts (FP8: as FP16, with 11 bits down
+ * to 2^-29 of the largest). requests = 0 is
  * allowed and does nothing. GEMV_ERR_UNSUPPORTED: more than 1,024 query heads
  * per key-value head; requests * kv_heads * (table_width * page_size / 16 + 2)
  * above 2,130,706,432.

@@ -232,6 +232,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     constexpr int H = NB * 8;             // query heads of a piece
     constexpr float kNegInf = -INFINITY;
     constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+    // Weights that meet V as FP16 are kept times 2^15 (the largest is 1): below 2^-14 FP16 has fewer bits.
+    constexpr float kUp = FP8 ? 15.f : 0.f, kDown = FP8 ? 0x1p-15f : 1.f;
 
     // A piece of a row: slices s .. s + seg - 1 of ns, the first of them slice `at` of the CTA's range.
     struct Piece {
@@ -828,12 +830,12 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[mt][j] = exp2_ftz(x[mt][j] - base[j & 1]);
+                    for (int j = 0; j < 4; ++j) x[mt][j] = exp2_ftz(x[mt][j] - (base[j & 1] - kUp));
                     l[nb][0] += x[mt][0] + x[mt][2];
                     l[nb][1] += x[mt][1] + x[mt][3];
-                    // P as the B operand. FP16 beside an FP8 cache (2^-12 relative). Beside a BF16 cache P has to
-                    // be BF16, whose 2^-9 would double the rounding error of a BF16 output: it goes in two parts
-                    // (the rest in a second BF16), 2^-18 together.
+                    // P as the B operand. FP16 beside an FP8 cache (2^-11 relative, down to 2^-29 of the largest
+                    // weight). Beside a BF16 cache P has to be BF16, whose 2^-8 would double the rounding error of
+                    // a BF16 output: it goes in two parts (the rest in a second BF16), 2^-17 together.
                     if constexpr (FP8) {
                         pb[mt][nb][0] = transpose8x8(pack_f16(x[mt][0], x[mt][1]));
                         pb[mt][nb][1] = transpose8x8(pack_f16(x[mt][2], x[mt][3]));
@@ -938,7 +940,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     inv[j] = l[nb][j] == 0.f ? 0.f : v_scale / l[nb][j];
                     if (p.lse && g == 0 && hd < nh)
                         p.lse[static_cast<int64_t>(row) * p.q_heads + head_at + hd] =
-                            m[nb][j] == kNegInf ? kNegInf : (m[nb][j] + log2f(l[nb][j])) * kLn2;
+                            m[nb][j] == kNegInf ? kNegInf : (m[nb][j] + log2f(l[nb][j] * kDown)) * kLn2;
                 }
                 // Transposed again, lane (g, t) holds columns 2t, 2t + 1 of the tile's rows for head g.
                 uint16_t* const o = p.out + static_cast<int64_t>(row) * p.out_stride + (head_at + nb * 8 + g) * p.head_dim;
@@ -998,7 +1000,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         const float inv = sum == 0.f ? 0.f : scale / sum;
         *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * p.out_stride + head * p.head_dim + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (p.lse && d == 0) p.lse[static_cast<int64_t>(row) * p.q_heads + head] = top == kNegInf ? kNegInf : (top + log2f(sum)) * kLn2;
+        if (p.lse && d == 0)
+            p.lse[static_cast<int64_t>(row) * p.q_heads + head] =
+                top == kNegInf ? kNegInf : (top + log2f(sum * kDown)) * kLn2;
     };
     const int d4s = p.head_dim / 4, items = nh * d4s;
     // Every warp finds the rows among the pieces by itself: lane i holds piece i.

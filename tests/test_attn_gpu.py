@@ -278,3 +278,33 @@ def test_rows_of_one_length_in_groups_of_sixteen_and_wide_heads():
     run([2500] * 3, 32, 2, 256, 24, "bf16", "head")
     run([2500] * 3, 64, 4, 128, 16, "bf16", "token")
     run([2500] * 3, 66, 2, 128, 16, "fp8", "token")             # 33 heads a group: two tiles of them, teams of 2
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_small_weights_beside_a_large_one(kind):
+    """One token takes nearly all the weight and has v = 0, so that the output is made of the others' weights alone:
+    2^-9 down to 2^-24 of its own."""
+    n, D, heads, G = 40, 64, 1, 4
+    cache = au.Cache([n], 16, heads, D, kind, seed=12)
+    one = 0x38 if kind == "fp8" else 1.0                       # the E4M3 code of 1
+    for which in range(2):
+        view = cache.view(which)
+        for j in range(n):
+            at = view[int(cache.table[0, j // 16]), j % 16, 0]
+            if which == 0:
+                at[:] = 0                                      # k = (j's part of the score, 0, ..)
+                cache.values[0][0][j, 0] = 0.0
+                if j == 7:
+                    at[0] = one
+                    cache.values[0][0][j, 0, 0] = 1.0 if kind == "bf16" else float(cache.scales[0][0])
+            elif j == 7:
+                at[:] = 0
+                cache.values[1][0][j, 0] = 0.0
+    k0 = float(cache.values[0][0][7, 0, 0])
+    q = torch.zeros(1, heads * G, D, dtype=torch.bfloat16)
+    for h, drop in enumerate((9.0, 14.0, 17.5, 24.0)):          # the large weight is 2^drop of the others'
+        q[0, h, 0] = drop * math.log(2.0) / k0
+    a = au.Attn([n], cache, heads * G, q=q.cuda(), scale=1.0)
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
