@@ -645,7 +645,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             }
             if constexpr (FP8) {
                 // The FP8 cache is widened to FP16 (exact); q is brought to FP16 by a power of two per head
-                // that puts its largest value in [1, 2): what that loses is below 2^-24 of that value.
+                // that puts its largest value in [2^14, 2^15): what that loses is below 2^-38 of that value.
                 float top = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
@@ -655,7 +655,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 int e = static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127;
-                e = top > 0.f ? max(-126, min(126, e)) : 0;
+                e = (top > 0.f ? max(-112, min(127, e)) : 0) - 14;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)

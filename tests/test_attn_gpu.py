@@ -308,3 +308,21 @@ def test_small_weights_beside_a_large_one(kind):
     a.run()
     torch.cuda.synchronize()
     a.check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("drop", [10, 17, 24])
+def test_small_queries_beside_a_large_one(kind, drop):
+    """A column where q is large and every k is 0: the scores are made of columns 2^-drop of it, in full precision."""
+    n, D = 50, 64
+    cache = au.Cache([n], 16, 1, D, kind, seed=13)
+    view = cache.view(0)
+    for j in range(n):
+        view[int(cache.table[0, j // 16]), j % 16, 0, 5] = 0
+        cache.values[0][0][j, 0, 5] = 0.0
+    q = (au.randn(3, 1, 4, D, device="cpu") * 2.0 ** -drop).bfloat16()
+    q[..., 5] = 3.0
+    a = au.Attn([n], cache, 4, q=q.cuda(), scale=0.25 * 2.0 ** drop)
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
