@@ -296,6 +296,8 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.group = group;
     p.qtiles = l.qtiles;
     p.team_shift = l.team_shift;
+    p.row_ctas = static_cast<int32_t>((l.grid / l.qtiles >> l.team_shift) /
+                                      (static_cast<int64_t>(a->requests) * (c->kv_heads >> l.team_shift)));
     p.head_dim = c->head_dim;
     p.page_size = c->page_size;
     p.table_width = a->table_width;
@@ -316,7 +318,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
         const int line = l.dt * es < 128 ? l.dt : static_cast<int>(128 / es);
         p.tma = gemv::api_encode_pool(&p.kmap, c->k, fp8, dims, st, line, rows) &&
                 gemv::api_encode_pool(&p.vmap, c->v, fp8, dims, st, line, rows);
-        p.box_rows = rows;
+        p.box_shift = shift_of(rows);
     }
     p.scale = a->scale;
     p.softcap = a->softcap;

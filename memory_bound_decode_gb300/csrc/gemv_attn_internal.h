@@ -60,8 +60,9 @@ struct AttnParams {
     int32_t requests, q_heads, kv_heads, group, qtiles, team_shift;
     int32_t head_dim, page_size, table_width, num_pages, window, max_len;
     int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
-    int32_t tma;                // 1: tensor copies of box_rows slots
-    int32_t box_rows;
+    int32_t tma;                // 1: tensor copies of 1 << box_shift slots
+    int32_t box_shift;
+    int32_t row_ctas;           // CTAs for each row where all rows are of one length; 0: too many rows
     float scale, softcap;
 };
 

@@ -351,25 +351,29 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // At least a slice per warp. Rows of up to two per warp are better not cut between CTAs, and of up to four if
     // that leaves work for a quarter of the CTAs: the slices of a warp come 1.3 us after each other, a join across
     // CTAs takes 4 (8 x 1,000 tokens: 12.6 us against 16.0; 1 x 1,000: 11.9 against 10.3).
-    const bool uncut = longest <= 2 * W || (longest <= 4 * W && total / longest * 4 >= ctas);
+    const bool uncut = longest <= 2 * W || (longest <= 4 * W && static_cast<int64_t>(total) * 4 >= static_cast<int64_t>(longest) * ctas);
     int quota = max((total + ctas - 1) / ctas, max(W, uncut ? longest : 0));
     // Rows of one length go to CTAs of their own where that adds no more than a slice per warp (a CTA between two rows
     // may be the last of both and join them one after the other: 1 x 8,000 tokens 17.7 us, so 15.0), or where a warp
     // has up to 16 slices (a join less: 13 x 2,000 tokens 26.0 -> 22.6 us, 16 x 4,000 48.0 -> 44.4; but 10 x 4,000
     // 34.2 -> 35.8).
-    int per_row = 0;                                                 // CTAs of a row, or 0
-    if (alike && !uncut && total > 0 && total / longest <= ctas) {
-        const int most = ctas / (total / longest), q = max(W, (longest + most - 1) / most);
+    int per_row = 0, f0 = 0, row_end = total;                        // CTAs of a row, or 0
+    int first_of_row = 0;                                            // its first CTA
+    if (alike && !uncut && total > 0 && p.row_ctas > 0) {
+        const int q = max(W, (longest + p.row_ctas - 1) / p.row_ctas);
         if (q <= max(quota + W, 16 * W)) {
             quota = q;
             per_row = (longest + q - 1) / q;
-            if (cta >= total / longest * per_row) return;
+            if (cta >= p.requests * blocks * per_row) return;
+            const int row = cta / per_row;
+            first_of_row = row * per_row;
+            f0 = row * longest + (cta - first_of_row) * q;
+            row_end = (row + 1) * longest;
         }
     }
-    const int in_row = per_row ? cta % per_row * quota : 0;
-    const int f0 = per_row ? cta / per_row * longest + in_row : cta * quota;   // below total + grid * quota
+    if (per_row == 0) f0 = cta * quota;                              // below total + grid * quota
     if (f0 >= total) return;
-    const int cnt = min(quota, per_row ? longest - in_row : total - f0);
+    const int cnt = min(quota, row_end - f0);
     const int part = (cnt + W - 1) / W;
     auto claim = [&](int r, int n, int end) {                        // `end`: slices up to request r, a head
         const int lo = (end - n) * blocks - f0, hi = end * blocks - f0;
@@ -445,7 +449,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     //
     // An entry holds the rows of a slice as lines of 128 bytes (one, two or four per row, each line's rows together)
     // with 16-byte chunk c of row r at c ^ (r & 7), the tensor copies' 128-byte swizzle; rows of 64 bytes with the
-    // 64-byte one. Tensor copies move boxes of box_rows slots of one page (box_rows divides page and slice), a
+    // 64-byte one. Tensor copies move boxes of slots of one page (a power of two that divides page and slice), a
     // lane per box and line. Where pages are no multiple of 8 slots, or lie outside this GPU's memory, every thread
     // copies 16-byte chunks.
     using Mask = std::conditional_t<TS == 64, uint64_t, uint32_t>;   // tokens of a slice
@@ -466,8 +470,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 
     // Pages are looked up for a batch of slices at a time, a lane per box (per token without tensor copies), and
     // a batch ahead: a look-up takes as long as all the copies in flight before it (3 us under load).
-    const int box = TMA ? p.box_rows : 1;
-    const int per_slice = TS / box, batch = 32 / per_slice;          // lanes a slice, slices a batch
+    const int box_shift = TMA ? p.box_shift : 0, box = 1 << box_shift;
+    const int per_slice = TS >> box_shift;                           // lanes a slice
+    const int slice_shift = 31 - __clz(per_slice), batch = 32 >> slice_shift;   // slices a batch
     struct Look {
         int r, h, s;                      // the slice
         int page, in;                     // in: the box's first slot in the page, -1 if no token of it is visible
@@ -481,7 +486,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     auto look_ahead = [&]() {             // `then` becomes the batch after it
         now = then;
         const int last = looked ? (batch - 1) * per_slice : 0;       // a lane of its last slice
-        const int idx = lane / per_slice;
+        const int idx = lane >> slice_shift;
         int ur = __shfl_sync(0xffffffffu, then.r, last), uh = __shfl_sync(0xffffffffu, then.h, last);
         int us = __shfl_sync(0xffffffffu, then.s, last) + 1 + idx;
         then.page = then.in = -1;
@@ -511,7 +516,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             then.r = ur;
             then.h = uh;
             then.s = us;
-            const int tok = first + lane % per_slice * box;
+            const int tok = first + ((lane & (per_slice - 1)) << box_shift);
             if (tok < len && tok + box > begin) {
                 const int blk = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
                 then.in = tok - blk * p.page_size;
@@ -562,7 +567,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     const int lines = TMA ? LINES : 1;
 #pragma unroll 1
                     for (int k = 0; k < TS; ++k)
-                        if (bad >> (k / box * lines) & 1u) last_valid &= ~(Mask(1) << k);
+                        if (bad >> ((k >> box_shift) * lines) & 1u) last_valid &= ~(Mask(1) << k);
                 }
                 if (lane == (issued & 31)) valid_of = last_valid;
                 if constexpr (TMA) {
@@ -1101,7 +1106,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // The first and last CTA of the row from before (lanes 0 and 1), of the one after (lanes 2 and 3).
     const Piece cut = lane < 2 ? before : after;
     const int row0 = f0 + cut.at - cut.s;                            // where it starts in the list
-    const int ends = per_row ? row0 / longest * per_row + (lane & 1 ? per_row - 1 : 0)
+    const int ends = per_row ? first_of_row + (lane & 1 ? per_row - 1 : 0)
                              : (row0 + (lane & 1 ? cut.ns - 1 : 0)) / quota;
     const int from0 = __shfl_sync(0xffffffffu, ends, 0), to0 = __shfl_sync(0xffffffffu, ends, 1);
     const int from1 = __shfl_sync(0xffffffffu, ends, 2), to1 = __shfl_sync(0xffffffffu, ends, 3);
