@@ -296,8 +296,10 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.group = group;
     p.qtiles = l.qtiles;
     p.team_shift = l.team_shift;
-    p.row_ctas = static_cast<int32_t>((l.grid / l.qtiles >> l.team_shift) /
-                                      (static_cast<int64_t>(a->requests) * (c->kv_heads >> l.team_shift)));
+    const int ctas = l.grid / l.qtiles >> l.team_shift;
+    p.row_ctas = static_cast<int32_t>(ctas / (static_cast<int64_t>(a->requests) * (c->kv_heads >> l.team_shift)));
+    p.cta_part = ctas > 1 ? ~uint64_t(0) / ctas + 1 : 0;      // 2^64 / ctas, rounded up
+    p.quarter_of = (1u << 20) / (c->head_dim / 4) + 1;
     p.head_dim = c->head_dim;
     p.page_size = c->page_size;
     p.table_width = a->table_width;

@@ -62,6 +62,8 @@ struct AttnParams {
     int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
     int32_t tma;                // 1: tensor copies of 1 << box_shift slots
     int32_t box_shift;
+    uint32_t quarter_of;        // x * quarter_of >> 20 is x / (head_dim / 4), up to 2,048
+    uint64_t cta_part;          // the upper half of n * cta_part is n / teams, up to 2^31 (0: one team)
     int32_t row_ctas;           // CTAs for each row where all rows are of one length; 0: too many rows
     float scale, softcap;
 };

@@ -255,13 +255,14 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int qt = blockIdx.x % p.qtiles;
+    // Integer divisions take long (0.05 us each, where everything waits for them): few are left.
+    const int unit = p.qtiles == 1 ? blockIdx.x : blockIdx.x / p.qtiles;
+    const int qt = blockIdx.x - unit * p.qtiles;
     // CTAs work in teams of 2, 4 or 8 where the KV heads divide into such blocks: the list is one of head blocks, and
     // each CTA of a team takes its own head of the block. They read neighbouring memory at the same time, and the HBM
     // gives more for it (FP8, 32 x 16,384 tokens: 220 -> 167 us; BF16, 64 x 32,768: 927 -> 884).
     const int blocks = p.kv_heads >> p.team_shift;
-    const int cta = blockIdx.x / p.qtiles >> p.team_shift, ctas = gridDim.x / p.qtiles >> p.team_shift;
-    const int member = blockIdx.x / p.qtiles & ((1 << p.team_shift) - 1);
+    const int cta = unit >> p.team_shift, member = unit & ((1 << p.team_shift) - 1);
     auto head_of = [&](int block) { return (block << p.team_shift) + member; };
     // The place in the grid of this team's CTA c (of this one's head).
     auto place_of = [&](int c) { return ((c << p.team_shift) + member) * p.qtiles + qt; };
@@ -351,8 +352,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // At least a slice per warp. Rows of up to two per warp are better not cut between CTAs, and of up to four if
     // that leaves work for a quarter of the CTAs: the slices of a warp come 1.3 us after each other, a join across
     // CTAs takes 4 (8 x 1,000 tokens: 12.6 us against 16.0; 1 x 1,000: 11.9 against 10.3).
-    const bool uncut = longest <= 2 * W || (longest <= 4 * W && static_cast<int64_t>(total) * 4 >= static_cast<int64_t>(longest) * ctas);
-    int quota = max((total + ctas - 1) / ctas, max(W, uncut ? longest : 0));
+    const uint64_t short_of = max(total - 1, 0);
+    const int even = static_cast<int>(p.cta_part ? __umul64hi(short_of, p.cta_part) : short_of) + 1;   // total / teams, up
+    const bool uncut = longest <= 2 * W || (longest <= 4 * W && even * 4 >= longest);
+    int quota = max(even, max(W, uncut ? longest : 0));
     // Rows of one length go to CTAs of their own where that adds no more than a slice per warp (a CTA between two rows
     // may be the last of both and join them one after the other: 1 x 8,000 tokens 17.7 us, so 15.0), or where a warp
     // has up to 16 slices (a join less: 13 x 2,000 tokens 26.0 -> 22.6 us, 16 x 4,000 48.0 -> 44.4; but 10 x 4,000
@@ -365,7 +368,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             quota = q;
             per_row = (longest + q - 1) / q;
             if (cta >= p.requests * blocks * per_row) return;
-            const int row = cta / per_row;
+            const int row = cta < per_row ? 0 : cta / per_row;
             first_of_row = row * per_row;
             f0 = row * longest + (cta - first_of_row) * q;
             row_end = (row + 1) * longest;
@@ -425,7 +428,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     int h = 0, s = 0;
     if (left > 0) {
         const int ns0 = max(1, attn_slices<TS>(p, len_of(r)));
-        h = off_r / ns0;
+        h = off_r < ns0 ? 0 : off_r / ns0;
         s = off_r - h * ns0;
     }
 
@@ -1010,6 +1013,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 top == kNegInf ? kNegInf : (top + log2f(sum * kDown)) * kLn2;
     };
     const int d4s = p.head_dim / 4, items = nh * d4s;
+    auto head_at = [&](int x) { return static_cast<int>(x * p.quarter_of >> 20); };   // x / d4s
     // Every warp finds the rows among the pieces by itself: lane i holds piece i.
     Piece own = {0, -1, -1, 0, 0, 0, 0, 0, 1.f};
     if (lane < 2 * W) own = s_piece[lane];
@@ -1053,7 +1057,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         float4 tail[UW];
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
-            const int x = u * T + tid, hd = x / d4s, d = (x - hd * d4s) * 4;
+            const int x = u * T + tid, hd = head_at(x), d = (x - hd * d4s) * 4;
             const float* from = j & 1 ? reinterpret_cast<const float*>(smem + (j >> 1) * kAttnRing) : first_piece(j >> 1);
             if (x < items) tail[u] = *reinterpret_cast<const float4*>(from + hd * DT + (d ^ (hd >> 1 & 3) * 8));
         }
@@ -1061,7 +1065,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         for (int u = 0; u < UW; ++u) {
             const int x = u * T + tid;
             if (x >= items) break;
-            const int hd = x / d4s, d = (x - hd * d4s) * 4;
+            const int hd = head_at(x), d = (x - hd * d4s) * 4;
             const int place = hd * DT + (d ^ (hd >> 1 & 3) * 8);
             const float2 ml_j = s_ml[j][hd];
             float2 ml[W - 1];
@@ -1106,8 +1110,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // The first and last CTA of the row from before (lanes 0 and 1), of the one after (lanes 2 and 3).
     const Piece cut = lane < 2 ? before : after;
     const int row0 = f0 + cut.at - cut.s;                            // where it starts in the list
-    const int ends = per_row ? first_of_row + (lane & 1 ? per_row - 1 : 0)
-                             : (row0 + (lane & 1 ? cut.ns - 1 : 0)) / quota;
+    int ends = first_of_row + (lane & 1 ? per_row - 1 : 0);
+    if (per_row == 0) ends = (row0 + (lane & 1 ? cut.ns - 1 : 0)) / quota;
     const int from0 = __shfl_sync(0xffffffffu, ends, 0), to0 = __shfl_sync(0xffffffffu, ends, 1);
     const int from1 = __shfl_sync(0xffffffffu, ends, 2), to1 = __shfl_sync(0xffffffffu, ends, 3);
     // One more arrival at a counter; whether it is the last of `all`, with the counter zero again for the next call.
@@ -1132,17 +1136,17 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     }
     __syncthreads();
 
-    // Joins the pieces of CTAs c0, c0 + step, .. up to `end` (the last one always `end`). Narrow tiles leave threads
-    // over: `parts` threads share an item then, each with every parts-th piece, and meet in the ring. B at a time,
+    // Joins the pieces of CTAs c0, c0 + 2^step_shift, .. up to `end` (the last one always `end`). Narrow tiles leave threads
+    // over: `parts` threads share an item then, each with every parts-th piece (from mine_of, past them: idle), and meet in the ring. B at a time,
     // all of whose loads are in flight together.
     constexpr int B = UW == 1 ? 5 : UW == 2 ? 8 : 4;
     const int parts = UW > 1 || 2 * items > T ? 1 : 4 * items > T ? 2 : 4;
-    const int mine_of = UW > 1 || tid < items ? 0 : tid / items;     // >= parts: idle
+    const int mine_of = UW > 1 ? 0 : (tid >= items) + (tid >= 2 * items) + (tid >= 3 * items) + (tid >= 4 * items);
     const int item = tid - mine_of * items;
     float top[UW], sum[UW];
     float4 o[UW];
-    auto join = [&](int from, int c0, int step, int end) {
-        const int count = (end - c0 + step - 1) / step + 1;
+    auto join = [&](int from, int c0, int step_shift, int end) {
+        const int count = ((end - c0 + (1 << step_shift) - 1) >> step_shift) + 1;
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
             top[u] = kNegInf;
@@ -1155,11 +1159,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             float4 v[B][UW];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const int at_b = b0 + b * parts, c = min(c0 + at_b * step, end);
+                const int at_b = b0 + b * parts, c = min(c0 + (at_b << step_shift), end);
                 const int at = (place_of(c) * 2 + (c == from ? 1 : 0)) * H;   // heads of pieces: below 2^31
 #pragma unroll
                 for (int u = 0; u < UW; ++u) {
-                    const int x = u * T + item, hd = x / d4s, d = (x - hd * d4s) * 4;
+                    const int x = u * T + item, hd = head_at(x), d = (x - hd * d4s) * 4;
                     ml[b][u] = make_float2(kNegInf, 0.f);
                     v[b][u] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (at_b < count && x < items) {
@@ -1215,7 +1219,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     auto store_row = [&](const Piece& a) {
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
-            const int x = u * T + tid, hd = x / d4s;
+            const int x = u * T + tid, hd = head_at(x);
             if (x < items) store(a.row, a.h, hd, (x - hd * d4s) * 4, o[u], top[u], sum[u], a.v_scale);
         }
     };
@@ -1223,7 +1227,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     for (int k = 0; k < 2; ++k) {
         if (s_last[k] != kLast) continue;
         const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1;
-        join(from, from, 1, to);
+        join(from, from, 0, to);
         store_row(k == 0 ? before : after);
     }
     if (s_last[0] != kGroups && s_last[1] != kGroups) return;
@@ -1232,18 +1236,18 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     for (int k = 0; k < 2; ++k) {
         if (!(k == 0 ? big[0] : big[1])) continue;
         const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1, n = to - from + 1;
-        const int g = n <= 64 ? 8 : n <= 256 ? 16 : 32, groups = (n + g - 1) / g;
-        const int begin = from + (cta - from) / g * g, end = min(begin + g - 1, to);
+        const int gs = n <= 64 ? 3 : n <= 256 ? 4 : 5, groups = (n + (1 << gs) - 1) >> gs;
+        const int begin = from + (cta - from >> gs << gs), end = min(begin + (1 << gs) - 1, to);
         // Groups are counted at their last CTA, which no other row's group ends at.
         __syncthreads();                                             // s_last has been read
         if (tid == 0) s_last[k] = arrive(p.ticket + kAttnTickets / 2 + place_of(end), end - begin + 1);
         __syncthreads();
         if (!s_last[k]) continue;
-        join(from, begin, 1, end);
+        join(from, begin, 0, end);
         __syncthreads();                                             // every thread has read the group's pieces
 #pragma unroll
         for (int u = 0; u < UW; ++u) {
-            const int x = u * T + tid, hd = x / d4s, d = (x - hd * d4s) * 4;
+            const int x = u * T + tid, hd = head_at(x), d = (x - hd * d4s) * 4;
             if (x >= items) break;
             const int64_t at = static_cast<int64_t>(place_of(end)) * 2 * H + hd;
             *reinterpret_cast<float4*>(p.part + at * DT + d) = o[u];
@@ -1253,7 +1257,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         if (tid == 0) s_last[k] = arrive(p.ticket + place_of(from), groups);
         __syncthreads();
         if (!s_last[k]) continue;
-        join(-1, from + g - 1, g, to);
+        join(-1, from + (1 << gs) - 1, gs, to);
         store_row(k == 0 ? before : after);
     }
 }

@@ -326,3 +326,16 @@ def test_small_queries_beside_a_large_one(kind, drop):
     a.run()
     torch.cuda.synchronize()
     a.check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("group, heads, dim", [(1024, 2, 256), (520, 4, 256), (1000, 1, 64)])
+def test_many_head_tiles_and_one_team(kind, group, heads, dim):
+    run([700, 3, 0, 2000], group * heads, heads, dim, 16, kind, "head")
+
+
+@pytest.mark.parametrize("dim", [8, 24, 40, 56, 88, 104, 136, 200, 216, 232, 240, 248])
+def test_head_sizes_cut_between_ctas(dim):
+    """Items of a join are numbered through heads of dim / 4 columns."""
+    run([9000], 7, 1, dim, 16)
+    run([2100, 300], 62, 2, dim, 16)
