@@ -32,7 +32,7 @@ namespace gemv {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 2;         // tokens whose rows a thread has in flight
+constexpr int kRopeTokens = 2;         // tokens whose rows a thread has in flight (at most 2)
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
     const int lane = threadIdx.y * blockDim.x + gi;
     for (int i = lane; i < tokens * half; i += blockDim.x * blockDim.y) {
-        const int t = TT == 1 ? 0 : i / half, pair = i - t * half;
+        const int t = TT > 1 && i >= half ? 1 : 0, pair = i - t * half;
         const int axis = p.pair_axis ? min(max(p.pair_axis[pair], 0), p.axes - 1) : 0;
         const int64_t pos = p.positions[axis * p.axis_stride + tok0 + t];
         const uint64_t turn = static_cast<uint64_t>(pos) * static_cast<uint64_t>(p.freqs[pair]);
