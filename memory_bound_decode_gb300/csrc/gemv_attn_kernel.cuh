@@ -30,11 +30,11 @@
 // operations, and the tensor pipe is 12-22% busy while the HBM is the limit.
 //
 // What bounds it. Long lists the HBM: 64 x 32,768 tokens of 8 heads of 128
-// (BF16) 884 us, 7.3 TB/s, 1.08 of a copy's rate; FP8, 32 requests of up to
-// 16,384 87 us, 6.2 TB/s. Groups of 16 heads of 256 columns the warps'
-// instructions (65 us for 46 us of bytes). Short ones latency: 1 x 1,000
-// tokens 10.6 us, of which the launch, the lengths, the page numbers and the
-// first tokens follow each other for 6, and the pieces' join takes 3.
+// (BF16) 882 us, 7.3 TB/s, 1.08 of a copy's rate; FP8, 32 requests of up to
+// 16,384 85 us, 6.3 TB/s. Groups of 16 heads of 256 columns the warps'
+// instructions (64 us for 46 us of bytes). Short ones latency: 1 x 1,000
+// tokens 8.7 us, of which the launch, the lengths, the page numbers and the
+// first tokens follow each other for 5, and the pieces' join takes 3.
 #pragma once
 
 #include <cstdint>
@@ -283,7 +283,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     }
     for (int i = lane; i < S::kRaw / 16; i += 32) reinterpret_cast<uint4*>(q_raw)[i] = make_uint4(0, 0, 0, 0);
     // The table into the L2, a line per thread of the grid (no matter who writes it before this call): a page number
-    // is needed as soon as the lengths are known. The lengths too, and the tensor copies' descriptions (0.2 us in all).
+    // is needed as soon as the lengths are known. The lengths too, and the tensor copies' descriptions (0.2 us).
     const int64_t line = (static_cast<int64_t>(blockIdx.x) * T + tid) * 32;
     if (line < p.requests * p.table_stride) prefetch_l2(p.table + line);
     if (tid * 32 < p.requests) prefetch_l2(p.lens + tid * 32);
@@ -351,9 +351,11 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     total *= blocks;                                                 // below 2^31: checked by the host
     // At least a slice per warp. Rows of up to two per warp are better not cut between CTAs, and of up to four if
     // that leaves work for a quarter of the CTAs: the slices of a warp come 1.3 us after each other, a join across
-    // CTAs takes 4 (8 x 1,000 tokens: 12.6 us against 16.0; 1 x 1,000: 11.9 against 10.3).
+    // CTAs takes 3 to 4 (measured before later steps: 8 x 1,000 tokens uncut 12.6 us, cut 14.4; 1 x 1,000 uncut 11.9,
+    // cut 10.3).
     const uint64_t short_of = max(total - 1, 0);
-    const int even = static_cast<int>(p.cta_part ? __umul64hi(short_of, p.cta_part) : short_of) + 1;   // total / teams, up
+    // total / teams, rounded up
+    const int even = static_cast<int>(p.cta_part ? __umul64hi(short_of, p.cta_part) : short_of) + 1;
     const bool uncut = longest <= 2 * W || (longest <= 4 * W && even * 4 >= longest);
     int quota = max(even, max(W, uncut ? longest : 0));
     // Rows of one length go to CTAs of their own where that adds no more than a slice per warp (a CTA between two rows
@@ -1136,9 +1138,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     }
     __syncthreads();
 
-    // Joins the pieces of CTAs c0, c0 + 2^step_shift, .. up to `end` (the last one always `end`). Narrow tiles leave threads
-    // over: `parts` threads share an item then, each with every parts-th piece (from mine_of, past them: idle), and meet in the ring. B at a time,
-    // all of whose loads are in flight together.
+    // Joins the pieces of CTAs c0, c0 + 2^step_shift, .. up to `end` (the last one always `end`). Narrow tiles leave
+    // threads over: `parts` threads share an item then, each with every parts-th piece (from mine_of, past them:
+    // idle), and meet in the ring. B at a time, all of whose loads are in flight together.
     constexpr int B = UW == 1 ? 5 : UW == 2 ? 8 : 4;
     const int parts = UW > 1 || 2 * items > T ? 1 : 4 * items > T ? 2 : 4;
     const int mine_of = UW > 1 ? 0 : (tid >= items) + (tid >= 2 * items) + (tid >= 3 * items) + (tid >= 4 * items);
@@ -1237,7 +1239,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         if (!(k == 0 ? big[0] : big[1])) continue;
         const int from = k == 0 ? from0 : from1, to = k == 0 ? to0 : to1, n = to - from + 1;
         const int gs = n <= 64 ? 3 : n <= 256 ? 4 : 5, groups = (n + (1 << gs) - 1) >> gs;
-        const int begin = from + (cta - from >> gs << gs), end = min(begin + (1 << gs) - 1, to);
+        const int begin = from + ((cta - from) >> gs << gs), end = min(begin + (1 << gs) - 1, to);
         // Groups are counted at their last CTA, which no other row's group ends at.
         __syncthreads();                                             // s_last has been read
         if (tid == 0) s_last[k] = arrive(p.ticket + kAttnTickets / 2 + place_of(end), end - begin + 1);

@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(kTableThreads) tables_kernel(const __grid_cons
     // Page numbers of a run are looked up together, then written together.
     const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kTableThreads * kRun;
-    for (int64_t tok = (static_cast<int64_t>(blockIdx.x) * kTableThreads + r) * kRun; tok < p.max_tokens; tok += stride) {
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * kTableThreads + r) * kRun;
+    for (int64_t tok = first; tok < p.max_tokens; tok += stride) {
         int of = request_of(p.requests, static_cast<uint32_t>(tok), [&](int i) { return s_first[i]; });
         int slot[kRun], position[kRun];
         const int32_t* from[kRun];
