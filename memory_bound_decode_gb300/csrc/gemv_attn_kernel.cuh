@@ -27,7 +27,7 @@
 // same lanes as its output columns. S^T becomes the B operand of the second
 // product by an 8x8 transposition in registers (movmatrix). These are the
 // warp-level MMAs: with 4 heads on a key-value head a byte of K or V takes 4
-// operations, and the tensor pipe is 12-22% busy while the HBM is the limit.
+// operations, and the tensor pipe is 13-23% busy while the HBM is the limit.
 //
 // What bounds it. Long lists the HBM: 64 x 32,768 tokens of 8 heads of 128
 // (BF16) 882 us, 7.3 TB/s, 1.08 of a copy's rate; FP8, 32 requests of up to
