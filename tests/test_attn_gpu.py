@@ -339,3 +339,16 @@ def test_head_sizes_cut_between_ctas(dim):
     """Items of a join are numbered through heads of dim / 4 columns."""
     run([9000], 7, 1, dim, 16)
     run([2100, 300], 62, 2, dim, 16)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("requests", [31, 32, 33, 255, 256, 257, 513])
+def test_counts_of_requests(kind, requests):
+    """Each warp, each CTA, or chunk after chunk sums the lengths up."""
+    lens = [(i * 37) % 211 if i % 9 else 0 for i in range(requests)]
+    lens[requests - 1] = 777
+    starts = [0]
+    for i in range(requests):
+        starts.append(starts[-1] + (0 if i % 11 == 3 else 1 + i % 2))
+    run(lens, 8, 2, 64, 16, kind, "token")
+    run(lens, 8, 2, 64, 16, kind, "head", token_start=starts, rows=starts[-1] + 1, window=100)
