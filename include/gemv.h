@@ -701,8 +701,9 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  *   table:  page numbers, table_width per request, as gemv_block_tables leaves
  *           them; entries past a request's last page are not read.
  * A request of length 0 gets zeros and lse -inf, as does one whose visible
- * tokens all lie in pages outside the pool (GEMV_STATUS_BAD_PAGE); one of
- * negative length is skipped, its rows left as they were.
+ * tokens all lie in pages outside the pool (GEMV_STATUS_BAD_PAGE), and a head
+ * whose scores are all -inf; one of negative length is skipped, its rows left
+ * as they were. A NaN score makes its head's outputs and lse NaN.
  *   workspace: gemv_attn_query's bytes, 16-byte aligned, zeroed once before its
  *           first use (every call leaves it fit for the next, of any shape that
  *           needs no more bytes). Calls that may run at the same time need a

@@ -948,9 +948,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 for (int j = 0; j < 2; ++j) {
                     const int hd = nb * 8 + 2 * t + j;
                     inv[j] = l[nb][j] == 0.f ? 0.f : v_scale / l[nb][j];
+                    // No weight: -inf. NaN scores, which no maximum shows, have made the sum NaN.
                     if (p.lse && g == 0 && hd < nh)
                         p.lse[static_cast<int64_t>(row) * p.q_heads + head_at + hd] =
-                            m[nb][j] == kNegInf ? kNegInf : (m[nb][j] + log2f(l[nb][j] * kDown)) * kLn2;
+                            (m[nb][j] + log2f(l[nb][j] * kDown)) * kLn2;
                 }
                 // Transposed again, lane (g, t) holds columns 2t, 2t + 1 of the tile's rows for head g.
                 uint16_t* const o = p.out + static_cast<int64_t>(row) * p.out_stride + (head_at + nb * 8 + g) * p.head_dim;
@@ -1011,8 +1012,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * p.out_stride + head * p.head_dim + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (p.lse && d == 0)
-            p.lse[static_cast<int64_t>(row) * p.q_heads + head] =
-                top == kNegInf ? kNegInf : (top + log2f(sum * kDown)) * kLn2;
+            p.lse[static_cast<int64_t>(row) * p.q_heads + head] = (top + log2f(sum * kDown)) * kLn2;
     };
     const int d4s = p.head_dim / 4, items = nh * d4s;
     auto head_at = [&](int x) { return static_cast<int>(x * p.quarter_of >> 20); };   // x / d4s
