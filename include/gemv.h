@@ -703,7 +703,8 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * A request of length 0 gets zeros and lse -inf, as does one whose visible
  * tokens all lie in pages outside the pool (GEMV_STATUS_BAD_PAGE), and a head
  * whose scores are all -inf; one of negative length is skipped, its rows left
- * as they were. A NaN score makes its head's outputs and lse NaN.
+ * as they were. A NaN score makes its head's outputs and lse NaN; a score of
+ * +inf makes its outputs NaN (inf / inf) and its lse +inf.
  *   workspace: gemv_attn_query's bytes, 16-byte aligned, zeroed once before its
  *           first use (every call leaves it fit for the next, of any shape that
  *           needs no more bytes). Calls that may run at the same time need a

@@ -157,6 +157,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// What scores are taken relative to: their maximum, or 0 where it is infinite (inf - inf would be NaN; so a score of
+// +inf has the weight inf, the sum is inf as it should be, and the outputs are inf / inf).
+__device__ __forceinline__ float base_of(float top) { return fabsf(top) == INFINITY ? 0.f : top; }
 __device__ __forceinline__ float low_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -822,8 +825,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     top = fmaxf(top, m[nb][j]);
-                    base[j] = top == kNegInf ? 0.f : top;
-                    corr[j] = exp2_ftz(m[nb][j] - base[j]);
+                    base[j] = base_of(top);
+                    corr[j] = top == INFINITY ? 1.f : exp2_ftz(m[nb][j] - base[j]);   // this lane's l may be 0
                     m[nb][j] = top;
                 }
                 l[nb][0] *= corr[0];
@@ -1077,7 +1080,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 ml[k] = k < n - 1 ? s_ml[i + 2 * k][hd] : make_float2(kNegInf, 0.f);
                 top = fmaxf(top, ml[k].x);
             }
-            const float base = top == kNegInf ? 0.f : top;
+            const float base = base_of(top);
             float e = exp2_ftz(ml_j.x - base);
             float sum = ml_j.y * e;
             float4 o = make_float4(tail[u].x * e, tail[u].y * e, tail[u].z * e, tail[u].w * e);
@@ -1179,7 +1182,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 float next = top[u];
 #pragma unroll
                 for (int b = 0; b < B; ++b) next = fmaxf(next, ml[b][u].x);
-                const float base = next == kNegInf ? 0.f : next, e = exp2_ftz(top[u] - base);
+                const float base = base_of(next), e = exp2_ftz(top[u] - base);
                 sum[u] *= e;
                 o[u] = make_float4(o[u].x * e, o[u].y * e, o[u].z * e, o[u].w * e);
                 top[u] = next;
@@ -1207,7 +1210,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             for (int k = 1; k < parts; ++k) {
                 const float2 ml = s_x[k * items + tid];
                 const float4 v = s_o[k * items + tid];
-                const float next = fmaxf(top[0], ml.x), base = next == kNegInf ? 0.f : next;
+                const float next = fmaxf(top[0], ml.x), base = base_of(next);
                 const float e = exp2_ftz(top[0] - base), f = exp2_ftz(ml.x - base);
                 top[0] = next;
                 sum[0] = sum[0] * e + ml.y * f;

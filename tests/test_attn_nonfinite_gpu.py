@@ -85,6 +85,21 @@ def test_nan_in_keys(lens, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("lens", LENGTHS)
+def test_infinite_scores(lens, kind):
+    """A score of +inf: its weight is inf / inf, so the outputs are NaN, and the sum of the exponentials is inf."""
+    a = make(lens, kind)
+    for r in range(0, len(lens), 2):
+        a.q[r, 5 * DIM + 11] = math.inf
+        if lens[r]:
+            put(a, 0, r, lens[r] - 1, 1, 11, 0x38 if kind == "fp8" else 1.0)
+    seen = check(a)
+    rows = sum(1 for r in range(0, len(lens), 2) if lens[r])
+    assert seen["lse_inf"] + seen["lse_nan"] == rows      # NaN where an FP8 key's code is 0
+    assert kind == "fp8" or seen["lse_inf"] == rows
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
 @pytest.mark.parametrize("lens", [[1], [40, 1, 0, 5], [3000]])
 def test_every_score_minus_infinity(lens, kind):
     a = make(lens, kind)
