@@ -705,6 +705,8 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * whose scores are all -inf; one of negative length is skipped, its rows left
  * as they were. A NaN score makes its head's outputs and lse NaN; a score of
  * +inf makes its outputs NaN (inf / inf) and its lse +inf.
+ * An infinite v makes its column infinite (NaN if the weight of its token is
+ * below 2^-110 of the largest, which counts as 0).
  *   workspace: gemv_attn_query's bytes, 16-byte aligned, zeroed once before its
  *           first use (every call leaves it fit for the next, of any shape that
  *           needs no more bytes). Calls that may run at the same time need a
@@ -714,8 +716,8 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * until that is zeroed again.
  * Products of BF16 (FP8: codes widened exactly to FP16, and q scaled into FP16
  * by a power of two per head) are summed in FP32, the softmax is kept in FP32;
- * the probabilities meet V as two BF16 parts (FP8: as FP16, with 11 bits down
- * to 2^-29 of the largest). requests = 0 is
+ * the probabilities, relative to the largest, meet V as two BF16 parts (2^-16;
+ * FP8: as FP16, with 11 bits down to 2^-29 of the largest). requests = 0 is
  * allowed and does nothing. GEMV_ERR_UNSUPPORTED: more than 1,024 query heads
  * per key-value head; requests * kv_heads * (table_width * page_size / 16 + 2)
  * above 2,130,706,432.

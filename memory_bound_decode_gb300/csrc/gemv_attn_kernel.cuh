@@ -152,6 +152,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ uint32_t pack_bf16_down(float lo, float hi) {   // towards zero
+    uint32_t r;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -848,12 +853,16 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     l[nb][1] += x[mt][1] + x[mt][3];
                     // P as the B operand. FP16 beside an FP8 cache (2^-11 relative, down to 2^-29 of the largest
                     // weight). Beside a BF16 cache P has to be BF16, whose 2^-8 would double the rounding error of
-                    // a BF16 output: it goes in two parts (the rest in a second BF16), 2^-17 together.
+                    // a BF16 output: it goes in two parts, the BF16 number below it and the rest in a second one,
+                    // 2^-16 together. Both are above zero (down to 2^-110 of the largest weight, where the rest
+                    // leaves BF16's range), so that an infinite v stays what it is: 0 * inf and inf - inf are NaN.
                     if constexpr (FP8) {
                         pb[mt][nb][0] = transpose8x8(pack_f16(x[mt][0], x[mt][1]));
                         pb[mt][nb][1] = transpose8x8(pack_f16(x[mt][2], x[mt][3]));
                     } else {
-                        const uint32_t a = pack_bf16(x[mt][0], x[mt][1]), b = pack_bf16(x[mt][2], x[mt][3]);
+                        constexpr float kBelow = 1.f - 0x1p-23f;                  // to the next FP32 number or two below
+                        const uint32_t a = pack_bf16_down(x[mt][0] * kBelow, x[mt][1] * kBelow);
+                        const uint32_t b = pack_bf16_down(x[mt][2] * kBelow, x[mt][3] * kBelow);
                         pb[mt][nb][0] = transpose8x8(a);
                         pb[mt][nb][1] = transpose8x8(b);
                         pl[mt][nb][0] = transpose8x8(pack_bf16(x[mt][0] - low_bf16(a), x[mt][1] - high_bf16(a)));

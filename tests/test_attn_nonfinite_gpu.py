@@ -84,6 +84,24 @@ def test_nan_in_keys(lens, kind):
     assert seen["lse_nan"] == GROUP * sum(n > 0 for n in lens)
 
 
+@pytest.mark.parametrize("lens", LENGTHS)
+@pytest.mark.parametrize("where", ["first", "last", "middle"])
+def test_infinite_values(lens, where):
+    """An infinite v makes its column infinite, of its own sign; both signs in a column make NaN."""
+    a = make(lens)
+    for r, n in enumerate(lens):
+        if n == 0:
+            continue
+        j = dict(first=0, last=n - 1, middle=n // 2)[where]
+        put(a, 1, r, j, 0, 3, math.inf)
+        put(a, 1, r, j, 0, 60, -math.inf)
+        put(a, 1, r, j, 1, 17, math.inf)
+        if n > 1:
+            put(a, 1, r, (j + 1) % n, 1, 17, -math.inf)
+    seen = check(a)
+    assert seen["inf"] >= GROUP and (max(lens) == 1 or seen["nan"])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 @pytest.mark.parametrize("lens", LENGTHS)
 def test_infinite_scores(lens, kind):
