@@ -587,7 +587,8 @@ typedef struct {
  *                   every later request that needs a page), 2 longer than its
  *                   row of table_width entries, 3 its tokens end past
  *                   max_tokens, 4 a negative length or count. A refused request
- *                   takes no pages; its tokens keep their numbers;
+ *                   takes no pages; its tokens keep their numbers, and
+ *                   gemv_attn_args.status keeps their old rows out of use;
  *   free_next_out   *free_next plus the pages taken.
  * new_lens may be lens and free_next_out may be free_next, so that a captured
  * call advances its own state; otherwise no output overlaps anything else.
@@ -700,6 +701,10 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  *           rows: rows that q and out have (read with token_start only).
  *   table:  page numbers, table_width per request, as gemv_block_tables leaves
  *           them; entries past a request's last page are not read.
+ *   status: NULL, or gemv_block_tables' array: a refused request (not 0) has a
+ *           query row that gemv_rope_append left as an earlier step wrote it.
+ *           It is not read; the request gets zeros and lse -inf, or is skipped
+ *           where its row is not below rows (refused for want of room).
  * A request of length 0 gets zeros and lse -inf, as does one whose visible
  * tokens all lie in pages outside the pool (GEMV_STATUS_BAD_PAGE), and a head
  * whose scores are all -inf; one of negative length is skipped, its rows left
@@ -728,6 +733,7 @@ typedef struct {
     float *lse;
     const int32_t *lens;
     const int32_t *token_start;
+    const int32_t *status;
     const int32_t *table;
     void *workspace;
     int64_t q_stride;

@@ -254,7 +254,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     if (a->token_start && (a->rows < 0 || a->rows > 0x7fffffffLL)) return GEMV_ERR_INVALID;
     if (a->q_stride % 4 != 0 || a->out_stride % 4 != 0 || !aligned(a->q, 8) || !aligned(a->out, 8) ||
         !aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(a->table, 4) || !aligned(a->token_start, 4) ||
-        !aligned(a->workspace, 16))
+        !aligned(a->status, 4) || !aligned(a->workspace, 16))
         return GEMV_ERR_ALIGN;
     // The kernel numbers the slices (16 tokens at least) of all rows in 31 bits.
     const int64_t reach = static_cast<int64_t>(a->table_width) * c->page_size;
@@ -272,6 +272,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.lse = a->lse;
     p.lens = a->lens;
     p.token_start = a->token_start;
+    p.status = a->status;
     p.rows = a->rows;
     p.table = a->table;
     p.kc = static_cast<const unsigned char*>(c->k);

@@ -45,6 +45,7 @@ struct AttnParams {
     float* lse;
     const int32_t* lens;
     const int32_t* token_start; // null: request r's query is row r
+    const int32_t* status;      // null: none; not 0: the request was refused a place for its new tokens
     const int32_t* table;
     const unsigned char* kc;
     const unsigned char* vc;

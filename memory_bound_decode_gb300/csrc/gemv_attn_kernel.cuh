@@ -176,19 +176,20 @@ __device__ __forceinline__ int attn_cut(const AttnParams& p, int len) {   // to 
     return p.max_len;
 }
 // Tokens of request r that its query can reach: its length, cut to what its
-// row of the table holds (with a status bit); 0 for an empty request, negative
-// for one that has no query row in this call.
+// row of the table holds (with a status bit); 0 for an empty or a refused
+// request, negative for one that has no query row in this call.
 static __device__ __noinline__ int attn_len(const AttnParams& p, int r) {
     const int len = p.lens[r];
+    const bool refused = p.status && p.status[r] != 0;
     if (p.token_start) {
         const int a = p.token_start[r], b = p.token_start[r + 1];
         if (b <= a) return -1;
         if (a < 0 || b > p.rows) {
-            atomicOr(&g_attn_status, kStatusBadPage);
+            if (!refused) atomicOr(&g_attn_status, kStatusBadPage);
             return -1;
         }
     }
-    return attn_cut(p, len);
+    return refused ? 0 : attn_cut(p, len);
 }
 __device__ __forceinline__ int attn_row(const AttnParams& p, int r) {
     return p.token_start ? p.token_start[r + 1] - 1 : r;
@@ -304,9 +305,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // every call; 1 x 1,000 tokens 10.7 -> 10.2).
     const bool few = p.requests <= 32;
     const int copy = few ? w * 32 : 0, first_of = tid - copy;        // this thread's request of the first chunk
-    const int len_first = first_of >= p.requests ? -1
-                          : p.token_start        ? attn_len(p, first_of)
-                                                 : attn_cut(p, p.lens[first_of]);
+    const int len_first = first_of >= p.requests      ? -1
+                          : p.token_start || p.status ? attn_len(p, first_of)
+                                                      : attn_cut(p, p.lens[first_of]);
     const int n_first = attn_slices<TS>(p, len_first);
     s_len[tid] = len_first;
     int incl = n_first;
@@ -344,7 +345,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         for (int i = 0; i < W; ++i) total += s_scan[i].x;
     }
 
-    // Requests without a visible token: zeros (nothing to average), from the CTA whose turn it is.
+    // Requests without a visible token, or refused: zeros (nothing to average), from the CTA whose turn it is.
     for (int r = blockIdx.x; r < p.requests; r += gridDim.x) {
         if ((r < T ? s_len[copy + r] : attn_len(p, r)) != 0) continue;
         const int row = attn_row(p, r);

@@ -292,7 +292,7 @@ class AttentionStep:
         d["attn"] = binding.attn_args(
             q=d["q"], out=d["out"], lens=self.new_lens, requests=B, q_heads=self.q_heads, q_stride=Q, out_stride=Q,
             table=self.table, table_width=self.width, table_stride=self.width, scale=D ** -0.5,
-            workspace=self.workspace, token_start=self.token_start, rows=B)
+            workspace=self.workspace, token_start=self.token_start, status=self.status, rows=B)
         d["segments"] = [(W, y, W.shape[0], self.ldw_h) for W, y in zip(d["W"], d["y"])]
         return d
 
