@@ -288,6 +288,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.q_stride = a->q_stride;
     p.out_stride = a->out_stride;
     p.table_stride = a->table_stride;
+    p.table_entries = gemv::attn_table_entries(a->requests, a->table_stride, a->table_width);
     p.page_stride = c->page_stride * elem_bytes(c);
     p.head_stride = c->head_stride * elem_bytes(c);
     p.slot_stride = c->slot_stride * elem_bytes(c);
@@ -303,7 +304,6 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     p.quarter_of = (1u << 20) / (c->head_dim / 4) + 1;
     p.head_dim = c->head_dim;
     p.page_size = c->page_size;
-    p.table_width = a->table_width;
     p.num_pages = c->num_pages;
     p.window = a->window;
     p.max_len = static_cast<int32_t>(reach);

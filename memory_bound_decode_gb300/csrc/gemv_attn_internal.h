@@ -38,6 +38,12 @@ constexpr int attn_slice(int dt, int nb, bool fp8, bool tma) {
     return (dt == 256 && (!fp8 || nb == 2)) || nb == 4 ? 16 : fp8 && nb == 1 && dt <= 128 && tma ? 64 : 32;
 }
 
+// Entries that a table of `width` per request, `stride` apart, reaches over:
+// what lies behind the last row's is not the caller's to name.
+constexpr int64_t attn_table_entries(int64_t requests, int64_t stride, int64_t width) {
+    return requests > 0 ? (requests - 1) * stride + width : 0;
+}
+
 struct AttnParams {
     CUtensorMap kmap, vmap;     // views of the pools, if tma
     const uint16_t* q;          // BF16
@@ -56,10 +62,11 @@ struct AttnParams {
     float* part_warp;           // a piece per warp, of rows cut between a CTA's warps
     uint32_t* ticket;
     int64_t q_stride, out_stride, table_stride;
+    int64_t table_entries;      // from the table's first to its last
     int64_t page_stride, head_stride, slot_stride;   // bytes
     int64_t rows;               // rows of q and out
     int32_t requests, q_heads, kv_heads, group, qtiles, team_shift;
-    int32_t head_dim, page_size, table_width, num_pages, window, max_len;
+    int32_t head_dim, page_size, num_pages, window, max_len;
     int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
     int32_t tma;                // 1: tensor copies of 1 << box_shift slots
     int32_t box_shift;

@@ -294,7 +294,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // The table into the L2, a line per thread of the grid (no matter who writes it before this call): a page number
     // is needed as soon as the lengths are known. The lengths too, and the tensor copies' descriptions (0.2 us).
     const int64_t line = (static_cast<int64_t>(blockIdx.x) * T + tid) * 32;
-    if (line < p.requests * p.table_stride) prefetch_l2(p.table + line);
+    if (line < p.table_entries) prefetch_l2(p.table + line);
     if (tid * 32 < p.requests) prefetch_l2(p.lens + tid * 32);
     if (TMA && lane == 0 && w < 2) prefetch_map(w == 0 ? &p.kmap : &p.vmap);
     __syncwarp();

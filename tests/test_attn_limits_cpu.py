@@ -1,4 +1,7 @@
 """Calls of the attention half that its front end refuses, beyond those of test_attn_cpu.py."""
+import os
+import subprocess
+
 import pytest
 
 from memory_bound_decode_gb300 import binding, build_lib
@@ -12,3 +15,21 @@ def built():
 
 def test_status_array_alignment():
     assert binding.gemv_attn_decode(attn(status=A16 + 2), cache(), 0, check=False) == ALIGN
+
+
+def evaluate(tmp_path, expressions):
+    """C++ expressions over the internal header, as whole numbers."""
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text('#include <cstdio>\n#include "gemv_attn_internal.h"\nint main() {\n'
+                   + "".join(f'std::printf("%lld\\n", static_cast<long long>({e}));\n' for e in expressions) + "}\n")
+    subprocess.run(["g++", "-std=c++17", "-I", build_lib.CSRC, "-I", os.path.join(build_lib.cuda_home(), "include"),
+                    str(src), "-o", str(exe)], check=True)
+    return [int(x) for x in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+
+
+def test_table_extent(tmp_path):
+    """What is asked into the L2 before the lengths are known ends with the last request's row, also where the rows
+    are a slice of wider ones; products in 64 bits."""
+    cases = [(1, 4, 4), (1, 100, 4), (3, 9, 2), (0, 5, 5), (1 << 30, 1 << 31, 7)]
+    got = evaluate(tmp_path, [f"gemv::attn_table_entries({r}LL, {s}LL, {w}LL)" for r, s, w in cases])
+    assert got == [max(0, r - 1) * s + w if r else 0 for r, s, w in cases]
