@@ -540,7 +540,8 @@ int gemv_probe_sink_words(void);
  *     g * page_stride + h * head_stride + s * slot_stride + d
  * so both usual orders ([pages][slots][heads][dim] and
  * [pages][heads][slots][dim]) and parts of a larger pool are strides. Strides
- * count elements and are multiples of 16 bytes; k and v are 16-byte aligned;
+ * count elements, are multiples of 16 bytes and at most 2^59; k and v are
+ * 16-byte aligned;
  * num_pages * page_size <= 2^31 - 1. Slot number g * page_size + s names slot
  * s of page g. What a slot holds that no length reaches is never part of a sum
  * (it may be NaN).

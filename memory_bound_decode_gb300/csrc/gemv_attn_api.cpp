@@ -25,11 +25,13 @@ int check_cache(const gemv_kv_cache* c) {
     const int unit = c->kind == GEMV_CACHE_FP8 ? 16 : 8;      // elements of a 16-byte access
     if (c->head_dim < unit || c->head_dim > GEMV_MAX_HEAD_DIM || c->head_dim % unit != 0) return GEMV_ERR_INVALID;
     const int64_t d = c->head_dim;
+    const int64_t most = int64_t(1) << 59;                     // so that no product below can wrap
+    if (c->page_stride > most || c->head_stride > most || c->slot_stride > most) return GEMV_ERR_INVALID;
     if ((c->num_pages > 1 && c->page_stride < d) || (c->kv_heads > 1 && c->head_stride < d) ||
         (c->page_size > 1 && c->slot_stride < d) || c->page_stride < 0 || c->head_stride < 0 || c->slot_stride < 0)
         return GEMV_ERR_INVALID;
     if (!fits(c->num_pages, 2 * c->page_stride) || !fits(c->kv_heads, 2 * c->head_stride) ||
-        !fits(c->page_size, 2 * c->slot_stride) || c->page_stride > (int64_t(1) << 59))
+        !fits(c->page_size, 2 * c->slot_stride))
         return GEMV_ERR_INVALID;
     if (c->kind == GEMV_CACHE_BF16 && (c->k_scale || c->v_scale)) return GEMV_ERR_INVALID;
     if (c->page_stride % unit != 0 || c->head_stride % unit != 0 || c->slot_stride % unit != 0 || !aligned(c->k, 16) ||

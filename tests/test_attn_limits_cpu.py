@@ -5,7 +5,7 @@ import subprocess
 import pytest
 
 from memory_bound_decode_gb300 import binding, build_lib
-from tests.test_attn_cpu import A16, ALIGN, attn, cache
+from tests.test_attn_cpu import A16, ALIGN, INVALID, attn, cache, rope
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -33,3 +33,18 @@ def test_table_extent(tmp_path):
     cases = [(1, 4, 4), (1, 100, 4), (3, 9, 2), (0, 5, 5), (1 << 30, 1 << 31, 7)]
     got = evaluate(tmp_path, [f"gemv::attn_table_entries({r}LL, {s}LL, {w}LL)" for r, s, w in cases])
     assert got == [max(0, r - 1) * s + w if r else 0 for r, s, w in cases]
+
+
+@pytest.mark.parametrize("kind", [binding.GEMV_CACHE_BF16, binding.GEMV_CACHE_FP8])
+@pytest.mark.parametrize("name", ["page_stride", "head_stride", "slot_stride"])
+@pytest.mark.parametrize("stride", [1 << 60, 1 << 61, 1 << 62, (1 << 63) - 16])
+@pytest.mark.parametrize("one", [False, True])
+def test_strides_whose_products_wrap(kind, name, stride, one):
+    """Twice 2^62 wraps to a negative number, which is below any bound. One page, head or slot makes no difference."""
+    f = {name: stride, "kind": kind}
+    if one:
+        f.update(num_pages=1, page_size=1)
+    c = cache(**f)
+    assert binding.gemv_attn_decode(attn(), c, 0, check=False) == INVALID
+    r = rope(v=A16, v_stride=128, slots=A16)
+    assert binding.gemv_rope_append(r, c, 0, check=False) == INVALID
