@@ -713,9 +713,10 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * +inf makes its outputs NaN (inf / inf) and its lse +inf.
  * An infinite v makes its column infinite (NaN if the weight of its token is
  * below 2^-110 of the largest, which counts as 0).
- *   workspace: gemv_attn_query's bytes, 16-byte aligned, zeroed once before its
- *           first use (every call leaves it fit for the next, of any shape that
- *           needs no more bytes). Calls that may run at the same time need a
+ *   workspace: workspace_bytes of device memory, at least gemv_attn_query's
+ *           for the call's shape (GEMV_ERR_INVALID if fewer), 16-byte aligned,
+ *           zeroed once before its first use (every call leaves it fit for the
+ *           next, of any shape that needs no more bytes). Calls that may run at the same time need a
  *           workspace each, replayed graphs among them.
  * What lens, token_start and table hold must not change while a call runs:
  * its results are then undefined, and so are later ones with its workspace
@@ -741,6 +742,7 @@ typedef struct {
     int64_t out_stride;
     int64_t table_stride;
     int64_t rows;
+    int64_t workspace_bytes;
     int32_t requests;
     int32_t q_heads;
     int32_t table_width;

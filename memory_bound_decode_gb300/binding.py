@@ -120,7 +120,7 @@ class gemv_rope_args(ctypes.Structure):
 
 class gemv_attn_args(ctypes.Structure):
     _fields_ = ([(n, vp) for n in ("q", "out", "lse", "lens", "token_start", "status", "table", "workspace")]
-                + [(n, i64) for n in ("q_stride", "out_stride", "table_stride", "rows")]
+                + [(n, i64) for n in ("q_stride", "out_stride", "table_stride", "rows", "workspace_bytes")]
                 + [(n, i32) for n in ("requests", "q_heads", "table_width", "window")]
                 + [("scale", ctypes.c_float), ("softcap", ctypes.c_float)])
 
@@ -453,12 +453,15 @@ def rope_args(*, q, k, q_out, positions, freqs, tokens: int, q_heads: int, kv_he
 
 def attn_args(*, q, out, lens, requests: int, q_heads: int, q_stride: int, out_stride: int, table, table_width: int,
               table_stride: int, scale: float, workspace, lse=None, token_start=None, status=None,
-              rows: int = 0, softcap: float = 0.0, window: int = 0) -> gemv_attn_args:
+              rows: int = 0, softcap: float = 0.0, window: int = 0, workspace_bytes: int | None = None) -> gemv_attn_args:
+    """``workspace_bytes``: the workspace's own size unless given; an address needs it."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.nbytes
     return _record(gemv_attn_args,
                    dict(q=q, out=out, lse=lse, lens=lens, token_start=token_start, status=status, table=table,
                         workspace=workspace),
                    dict(q_stride=q_stride, out_stride=out_stride, table_stride=table_stride, rows=rows,
-                        requests=requests, q_heads=q_heads, table_width=table_width, window=window, scale=scale,
+                        workspace_bytes=workspace_bytes, requests=requests, q_heads=q_heads, table_width=table_width, window=window, scale=scale,
                         softcap=softcap))
 
 

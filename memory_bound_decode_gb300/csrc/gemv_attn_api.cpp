@@ -263,11 +263,15 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     if (reach > 0x7fffff00LL || static_cast<double>(reach / 16 + 2) * a->requests * c->kv_heads > 0x7f000000)
         return GEMV_ERR_UNSUPPORTED;
     if (a->requests == 0) return GEMV_OK;
-    int sm_count = 0;
-    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
     gemv::AttnLaunch l = {};
     const int fp8 = c->kind == GEMV_CACHE_FP8;
+    // What a GPU of one SM needs, so that a size left out is refused where there is none; then what this one needs.
+    if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, fp8, 1, &l)) != GEMV_OK) return rc;
+    if (a->workspace_bytes < l.workspace_bytes) return GEMV_ERR_INVALID;
+    int sm_count = 0;
+    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
     if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, fp8, sm_count, &l)) != GEMV_OK) return rc;
+    if (a->workspace_bytes < l.workspace_bytes) return GEMV_ERR_INVALID;
     gemv::AttnParams p = {};
     p.q = static_cast<const uint16_t*>(a->q);
     p.out = static_cast<uint16_t*>(a->out);

@@ -3,6 +3,7 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 from memory_bound_decode_gb300 import binding, build_lib
 from tests.test_attn_cpu import A16, ALIGN, INVALID, attn, cache, rope
@@ -48,3 +49,18 @@ def test_strides_whose_products_wrap(kind, name, stride, one):
     assert binding.gemv_attn_decode(attn(), c, 0, check=False) == INVALID
     r = rope(v=A16, v_stride=128, slots=A16)
     assert binding.gemv_rope_append(r, c, 0, check=False) == INVALID
+
+
+@pytest.mark.parametrize("kind", [binding.GEMV_CACHE_BF16, binding.GEMV_CACHE_FP8])
+def test_workspace_too_small(kind):
+    """Refused on the host: an address without a size, a negative one, one below what a single CTA needs."""
+    need = binding.gemv_attn_query(8, 2, 64, kind, 1)["workspace_bytes"]
+    for over in (dict(), dict(workspace_bytes=0), dict(workspace_bytes=-1), dict(workspace_bytes=need - 1)):
+        assert binding.gemv_attn_decode(attn(**over), cache(kind=kind), 0, check=False) == INVALID
+
+
+def test_workspace_size_of_a_tensor():
+    for n in (4096, 100):
+        assert attn(workspace=torch.zeros(n, dtype=torch.uint8)).workspace_bytes == n
+    assert attn(workspace=torch.zeros(64, dtype=torch.float32)).workspace_bytes == 256
+    assert attn(workspace_bytes=7).workspace_bytes == 7
