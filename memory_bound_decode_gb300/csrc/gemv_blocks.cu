@@ -104,7 +104,8 @@ __device__ __forceinline__ void sum_chunk(const TablesParams& p, Request& q, boo
         q.first = sat_add(sums.tokens, sat_add(tok_ex, w > 0 ? tw : 0));
         q.page_first = sat_add(sums.pages, sat_add(page_ex, w > 0 ? gw : 0));
         if (again) break;
-        const bool over = q.state == kServed && count > 0 && sat_add(q.first, count) > p.max_tokens;
+        // (In 64 bits: where max_tokens is kMax itself, a saturated sum would not be above it.)
+        const bool over = q.state == kServed && count > 0 && static_cast<int64_t>(q.first) + count > p.max_tokens;
         if (over) {
             q.state = kNoRoom;
             need = 0;
