@@ -593,8 +593,8 @@ typedef struct {
  *   free_next_out   *free_next plus the pages taken.
  * new_lens may be lens and free_next_out may be free_next, so that a captured
  * call advances its own state; otherwise no output overlaps anything else.
- * max_tokens >= 1; table_width * page_size and num_pages * page_size at most
- * 2^31 - 1. All arrays are int32, 4-byte aligned.
+ * requests <= 2^30; max_tokens >= 1; table_width * page_size and num_pages *
+ * page_size at most 2^31 - 1. All arrays are int32, 4-byte aligned.
  */
 typedef struct {
     const int32_t *lens;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from memory_bound_decode_gb300 import binding, build_lib
-from tests.test_attn_cpu import A16, ALIGN, INVALID, attn, cache, rope
+from tests.test_attn_cpu import A16, ALIGN, INVALID, attn, cache, rope, tables
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -64,3 +64,8 @@ def test_workspace_size_of_a_tensor():
         assert attn(workspace=torch.zeros(n, dtype=torch.uint8)).workspace_bytes == n
     assert attn(workspace=torch.zeros(64, dtype=torch.float32)).workspace_bytes == 256
     assert attn(workspace_bytes=7).workspace_bytes == 7
+
+
+@pytest.mark.parametrize("requests", [(1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1])
+def test_more_requests_than_are_counted(requests):
+    assert binding.gemv_block_tables(tables(requests=requests), 0, check=False) == INVALID
