@@ -52,6 +52,7 @@ struct Workspace {
 
 struct DeviceState {
     bool ready = false;
+    bool attn_ready = false;   // the attention kernels too: on the first attention call, which only they serve
     int status = GEMV_OK;
     int sm_count = 0;
     int32_t tc_clusters[4] = {-1, -1, -1, -1};   // resident clusters of 1, 2, 4, 8 tcgen05 CTAs
@@ -78,7 +79,7 @@ int device_state(int* sm_count) {
             return cuda_fail(e);
         if (major != 10 || minor != 3) {
             st.status = GEMV_ERR_UNSUPPORTED;
-        } else if ((e = gemv::prepare_kernels(dev)) != cudaSuccess || (e = gemv::prepare_attn()) != cudaSuccess) {
+        } else if ((e = gemv::prepare_kernels(dev)) != cudaSuccess) {
             return cuda_fail(e);
         } else {
             st.status = GEMV_OK;
@@ -89,6 +90,17 @@ int device_state(int* sm_count) {
     }
     *sm_count = st.sm_count;
     return st.status;
+}
+
+// Whether the current device's attention kernels have been set up (and so may have recorded a status).
+bool attn_in_use() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return false;
+    }
+    std::lock_guard<std::mutex> lock(g_dev_mutex);
+    return g_dev[dev].attn_ready;
 }
 
 // The current device's resident-cluster counts for the tcgen05 kernel (set
@@ -621,6 +633,20 @@ bool plan_is_independent(const gemv_proj* projs, int nproj, const std::vector<si
 namespace gemv {
 
 int api_device_state(int* sm_count) { return device_state(sm_count); }
+
+// The same, with the attention kernels' shared-memory limits raised. Setting them up with the GEMVs' would cost every
+// process 2.8 ms of its first GEMV call (4.2 -> 7.0 ms), and its failure that call.
+int api_attn_state(int* sm_count) {
+    int rc = device_state(sm_count), dev = 0;
+    if (rc != GEMV_OK) return rc;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    std::lock_guard<std::mutex> lock(g_dev_mutex);
+    if (!g_dev[dev].attn_ready && (e = prepare_attn()) != cudaSuccess) return cuda_fail(e);
+    g_dev[dev].attn_ready = true;
+    return GEMV_OK;
+}
+
 int api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
 bool api_pdl_enabled() { return pdl_enabled(); }
 bool api_on_current_device(const void* p) { return on_current_device(p); }
@@ -1173,7 +1199,7 @@ int gemv_device_status(unsigned int* bits, int reset) {
     if (e == cudaSuccess) e = gemv::read_mma_status_nb2(&b3, reset != 0);
     if (e == cudaSuccess) e = gemv::read_fp8_status(&b4, reset != 0);
     if (e == cudaSuccess) e = gemv::read_tc_status(&b5, reset != 0);
-    if (e == cudaSuccess) e = gemv::read_attn_status(&b6, reset != 0);
+    if (e == cudaSuccess && attn_in_use()) e = gemv::read_attn_status(&b6, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e);
     *bits = b1 | b2 | b3 | b4 | b5 | b6;
     return GEMV_OK;

@@ -271,7 +271,7 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, fp8, 1, &l)) != GEMV_OK) return rc;
     if (a->workspace_bytes < l.workspace_bytes) return GEMV_ERR_INVALID;
     int sm_count = 0;
-    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
+    if ((rc = gemv::api_attn_state(&sm_count)) != GEMV_OK) return rc;
     if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, fp8, sm_count, &l)) != GEMV_OK) return rc;
     if (a->workspace_bytes < l.workspace_bytes) return GEMV_ERR_INVALID;
     gemv::AttnParams p = {};

@@ -12,6 +12,7 @@ namespace gemv {
 
 // ---- shared with gemv_api.cpp -------------------------------------------------
 int api_device_state(int* sm_count);      // set-up of the current device; GEMV_OK or an error
+int api_attn_state(int* sm_count);        // and of its attention kernels
 int api_cuda_fail(cudaError_t e);         // record e for gemv_last_cuda_error; GEMV_ERR_CUDA
 bool api_pdl_enabled();
 bool api_on_current_device(const void* p);   // whether p points into the current device's own memory
