@@ -696,6 +696,8 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * reads key-value head i / (q_heads / kv_heads).
  *   q, out: BF16 rows of q_heads x head_dim values, strides in elements
  *           (multiples of 4), 8-byte aligned;  lse: [row][q_heads] FP32 or NULL.
+ *   scale, softcap: finite, softcap >= 0, and so are scale / softcap and both
+ *           times log2(e) in FP32.
  *   token_start NULL: request r's query is row r. Else (gemv_block_tables'
  *           array, requests + 1 entries) it is row token_start[r + 1] - 1, the
  *           last of its new tokens; a request without new tokens is skipped.

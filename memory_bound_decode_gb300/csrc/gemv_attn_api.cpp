@@ -255,6 +255,11 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
     if (a->table_width < 1 || a->table_stride < a->table_width || a->table_stride > most) return GEMV_ERR_INVALID;
     if (!std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0.f || a->window < 0)
         return GEMV_ERR_INVALID;
+    // The factors the kernel makes of them: an infinite one would turn a score of 0 into NaN.
+    const float log2e = 1.4426950408889634f;
+    if (!std::isfinite(a->softcap > 0.f ? a->scale / a->softcap : a->scale * log2e) ||
+        !std::isfinite(a->softcap * log2e))
+        return GEMV_ERR_INVALID;
     if (a->token_start && (a->rows < 0 || a->rows > 0x7fffffffLL)) return GEMV_ERR_INVALID;
     if (a->q_stride % 4 != 0 || a->out_stride % 4 != 0 || !aligned(a->q, 8) || !aligned(a->out, 8) ||
         !aligned(a->lse, 4) || !aligned(a->lens, 4) || !aligned(a->table, 4) || !aligned(a->token_start, 4) ||

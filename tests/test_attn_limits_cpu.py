@@ -9,6 +9,9 @@ from memory_bound_decode_gb300 import binding, build_lib
 from tests.test_attn_cpu import A16, ALIGN, INVALID, attn, cache, rope, tables
 
 
+ROOM = 1 << 40   # a workspace's size that does for any shape
+
+
 @pytest.fixture(scope="module", autouse=True)
 def built():
     build_lib.build()
@@ -46,7 +49,7 @@ def test_strides_whose_products_wrap(kind, name, stride, one):
     if one:
         f.update(num_pages=1, page_size=1)
     c = cache(**f)
-    assert binding.gemv_attn_decode(attn(), c, 0, check=False) == INVALID
+    assert binding.gemv_attn_decode(attn(workspace_bytes=ROOM), c, 0, check=False) == INVALID
     r = rope(v=A16, v_stride=128, slots=A16)
     assert binding.gemv_rope_append(r, c, 0, check=False) == INVALID
 
@@ -69,3 +72,10 @@ def test_workspace_size_of_a_tensor():
 @pytest.mark.parametrize("requests", [(1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1])
 def test_more_requests_than_are_counted(requests):
     assert binding.gemv_block_tables(tables(requests=requests), 0, check=False) == INVALID
+
+
+@pytest.mark.parametrize("over", [dict(scale=0.125, softcap=1e-40), dict(scale=-1.0, softcap=1e-45),
+                                  dict(scale=3e38), dict(scale=-3e38), dict(scale=1.0, softcap=3e38)])
+def test_factors_past_fp32(over):
+    """scale / softcap, or either in powers of two, is infinite in FP32: times a score of 0 it would be NaN."""
+    assert binding.gemv_attn_decode(attn(**over, workspace_bytes=ROOM), cache(), 0, check=False) == INVALID
