@@ -396,8 +396,8 @@ int gemv_workspace_release(void);
 
 /*
  * Status bits the kernels recorded on the current device since the last reset:
- * GEMV_STATUS_WAIT_TIMEOUT means a kernel gave up waiting for a copy of x into
- * shared memory (an mbarrier wait has an iteration limit instead of spinning
+ * GEMV_STATUS_WAIT_TIMEOUT means a kernel gave up waiting for a copy of x (the
+ * attention: of K, V or q) into shared memory (an mbarrier wait has an iteration limit instead of spinning
  * forever); the CTAs that gave up store NaN in place of their outputs, so a
  * timed-out launch never returns plausible numbers. The calls themselves still
  * return GEMV_OK (the wait happens on the device, after the call): a caller

@@ -50,6 +50,12 @@ namespace gemv {
 static __device__ unsigned int g_attn_status;
 constexpr unsigned int kStatusBadPage = 2u;   // kStatusWaitTimeout (1) too
 
+#ifdef GEMV_DEBUG_DROP_X
+constexpr bool kDropV = true;    // the test build whose waits are meant to run out: V is never copied
+#else
+constexpr bool kDropV = false;
+#endif
+
 namespace attn {
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -595,10 +601,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             if constexpr (TMA) {
                 if (lane == 0) expect_bytes(bar, S::kEntry);
                 __syncwarp();
-                if (lane < per_slice * LINES)
+                if (lane < per_slice * LINES && (kIsK || !kDropV))
                     copy_box(dst + lane % LINES * TS * 128 + lane / LINES * box * LB, kIsK ? &p.kmap : &p.vmap,
                              lane % LINES * (FP8 ? 128 : 64), box_in, box_h, box_page, bar, keep);
-            } else {
+            } else if (kIsK || !kDropV) {
                 copy_rows(kIsK ? p.kc : p.vc, dst);
                 copies_arrive(bar);
             }
