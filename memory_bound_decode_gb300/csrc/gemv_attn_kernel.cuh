@@ -967,6 +967,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 for (int j = 0; j < 2; ++j) {
                     const int hd = nb * 8 + 2 * t + j;
                     inv[j] = l[nb][j] == 0.f ? 0.f : v_scale / l[nb][j];
+                    if (l[nb][j] == 0.f) {                           // no weight at all: zeros, whatever v holds
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks) acc[ks][nb][j] = acc[ks][nb][j + 2] = 0.f;
+                    }
                     // No weight: -inf. NaN scores, which no maximum shows, have made the sum NaN.
                     if (p.lse && g == 0 && hd < nh)
                         p.lse[static_cast<int64_t>(row) * p.q_heads + head_at + hd] =
@@ -1028,6 +1032,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     auto store = [&](int row, int block, int hd, int d, float4 o, float top, float sum, float scale) {
         const int64_t head = static_cast<int64_t>(head_of(block)) * p.group + head0 + hd;
         const float inv = sum == 0.f ? 0.f : scale / sum;
+        if (sum == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
         *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * p.out_stride + head * p.head_dim + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (p.lse && d == 0)

@@ -127,3 +127,19 @@ def test_every_score_minus_infinity(lens, kind):
             put(a, 0, r, j, 0, 1, 0xB8 if kind == "fp8" else -1.0)
     seen = check(a)
     assert seen["none"] == sum(n > 0 for n in lens)
+
+
+@pytest.mark.parametrize("lens", [[1], [40, 1, 0, 5], [3000]])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_no_weight_beside_values_that_are_not_finite(lens, value):
+    """Zeros all the same: none of them has a weight in that head; in the others they count."""
+    a = make(lens)
+    for r, n in enumerate(lens):
+        a.q[r, 2 * DIM + 1] = math.inf
+        for j in range(n):
+            put(a, 0, r, j, 0, 1, -1.0)
+        if n:
+            put(a, 1, r, n // 2, 0, 20, value)
+    seen = check(a)
+    rows = sum(n > 0 for n in lens)
+    assert seen["none"] == rows and seen["nan"] == (rows * (GROUP - 1) if math.isnan(value) else 0)
