@@ -397,14 +397,14 @@ int gemv_workspace_release(void);
 /*
  * Status bits the kernels recorded on the current device since the last reset:
  * GEMV_STATUS_WAIT_TIMEOUT means a kernel gave up waiting for a copy of x (the
- * attention: of K, V or q) into shared memory (an mbarrier wait has an iteration limit instead of spinning
- * forever); the CTAs that gave up store NaN in place of their outputs, so a
- * timed-out launch never returns plausible numbers. The calls themselves still
- * return GEMV_OK (the wait happens on the device, after the call): a caller
- * that must know reads the bits after synchronizing. Writes the bits to
- * *bits and clears them when reset != 0. Synchronous with respect to the
- * device's work (like cudaMemcpyFromSymbol). Returns GEMV_OK, GEMV_ERR_INVALID
- * for a NULL pointer, or GEMV_ERR_CUDA.
+ * attention: of K, V or q) into shared memory (an mbarrier wait has an
+ * iteration limit instead of spinning forever); the CTAs that gave up store NaN
+ * in place of their outputs, so a timed-out launch never returns plausible
+ * numbers. The calls themselves still return GEMV_OK (the wait happens on the
+ * device, after the call): a caller that must know reads the bits after
+ * synchronizing. Writes the bits to *bits and clears them when reset != 0.
+ * Synchronous with respect to the device's work (like cudaMemcpyFromSymbol).
+ * Returns GEMV_OK, GEMV_ERR_INVALID for a NULL pointer, or GEMV_ERR_CUDA.
  */
 #define GEMV_STATUS_WAIT_TIMEOUT 1u
 /* GEMV_STATUS_BAD_PAGE: gemv_attn_decode met a page number outside the pool, a
@@ -718,9 +718,9 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  *   workspace: workspace_bytes of device memory, at least gemv_attn_query's
  *           for the call's shape (GEMV_ERR_INVALID if fewer), 16-byte aligned,
  *           zeroed once before its first use (every call leaves it fit for the
- *           next, of any shape that needs no more bytes). Calls that may run at the same time need a
- *           workspace each, replayed graphs among them.
- * What lens, token_start and table hold must not change while a call runs:
+ *           next, of any shape that needs no more bytes). Calls that may run
+ *           at the same time need a workspace each, replayed graphs among them.
+ * What lens, token_start, status and table hold must not change while a call runs:
  * its results are then undefined, and so are later ones with its workspace
  * until that is zeroed again.
  * Products of BF16 (FP8: codes widened exactly to FP16, and q scaled into FP16

@@ -90,10 +90,11 @@ def build_debug(force: bool = False, verbose: bool = False) -> str:
 
 def build_debug_drop_x(force: bool = False, verbose: bool = False) -> str:
     """The test build whose tcgen05 kernels never issue their copies of x, and
-    whose attention kernels never issue those of V: the barriers wait for
-    bytes that never come, so the bounded waits run out (limit 2^14 rounds in
-    this build) and the kernel takes its failure path: NaN outputs, the status
-    bit, its tensor memory freed."""
+    whose attention kernels never issue those of V (with tensor copies) or
+    never count their queries in: the barriers wait for what never comes, so
+    the bounded waits run out (limit 2^14 rounds in this build) and the kernel
+    takes its failure path: NaN outputs, the status bit, its tensor memory
+    freed."""
     return build(force=force, verbose=verbose, extra_flags=DROP_X_FLAGS, lib=LIB_DEBUG_DROP_X)
 
 

@@ -51,9 +51,10 @@ static __device__ unsigned int g_attn_status;
 constexpr unsigned int kStatusBadPage = 2u;   // kStatusWaitTimeout (1) too
 
 #ifdef GEMV_DEBUG_DROP_X
-constexpr bool kDropV = true;    // the test build whose waits are meant to run out: V is never copied
+constexpr bool kDrop = true;     // the test build whose waits are meant to run out: instances with tensor copies never
+                                 // copy V, the others never count their queries in
 #else
-constexpr bool kDropV = false;
+constexpr bool kDrop = false;
 #endif
 
 namespace attn {
@@ -462,7 +463,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             for (int i = lane; i < per; i += 32) copy8(to + hd * S::kRawStride + i * 8, src + (hd * per + i) * 8);
         if (FP8 && lane < 2 && (lane ? p.v_scale : p.k_scale))
             copy4(smem_addr(&s_scales[w][lane]), (lane ? p.v_scale : p.k_scale) + hk);
-        copies_arrive(smem_addr(&s_qbar[w]));
+        if (TMA || !kDrop) copies_arrive(smem_addr(&s_qbar[w]));
     };
 
     // ---- copies of K and V into this warp's ring: entries K0 V0 K1 V1 ..., E of them at a time ----
@@ -601,10 +602,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             if constexpr (TMA) {
                 if (lane == 0) expect_bytes(bar, S::kEntry);
                 __syncwarp();
-                if (lane < per_slice * LINES && (kIsK || !kDropV))
+                if (lane < per_slice * LINES && (kIsK || !kDrop))
                     copy_box(dst + lane % LINES * TS * 128 + lane / LINES * box * LB, kIsK ? &p.kmap : &p.vmap,
                              lane % LINES * (FP8 ? 128 : 64), box_in, box_h, box_page, bar, keep);
-            } else if (kIsK || !kDropV) {
+            } else {
                 copy_rows(kIsK ? p.kc : p.vc, dst);
                 copies_arrive(bar);
             }
@@ -652,7 +653,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     };
     float v_scale = 1.f;
     auto place_query = [&]() {
-        wait_phase(smem_addr(&s_qbar[w]), q_phase);                  // plain loads of this warp: they do land
+        ok = __all_sync(0xffffffffu, ok && wait_phase(smem_addr(&s_qbar[w]), q_phase)) != 0;
         q_phase ^= 1u;
         const float ksc = score_scale * (FP8 ? s_scales[w][0] : 1.f);
         v_scale = FP8 ? s_scales[w][1] : 1.f;

@@ -1,7 +1,8 @@
 """The failure path of the attention kernels, made to run on purpose without a fault: a test build (GEMV_DEBUG_DROP_X)
-never issues the copies of V, so a warp's first wait for them runs out (2^14 rounds in that build). Every row gets NaN,
-whoever finishes it: a warp, a CTA's join, the last CTA of a row, either level of a long row. The status bit is set, the
-workspace is left as a call leaves it, and the regular library computes right after, in the same process."""
+never issues the copies of V (in the kernels with tensor copies), or never counts a query's copies in (in the
+others), so a warp's first wait for them runs out (2^14 rounds in that build). Every row gets NaN, whoever finishes it: a
+warp, a CTA's join, the last CTA of a row, either level of a long row. The status bit is set, the workspace is left as a
+call leaves it, and the regular library computes right after, in the same process."""
 import math
 
 import pytest
