@@ -627,8 +627,9 @@ int gemv_block_tables(const gemv_block_tables_args *args, void *stream);
  *     positions[axis * axis_stride + t] * inv_freq[i],  axis = pair_axis[i]
  * (columns from rot_dim on are copied). With one axis pair_axis is unused and
  * may be NULL; images and video give each pair one of up to GEMV_MAX_AXES axes
- * (time, height, width). freqs holds inv_freq as gemv_rope_freqs makes it: the
- * angle is then reduced exactly however far the position is.
+ * (time, height, width). freqs holds inv_freq as gemv_rope_freqs makes it, to
+ * 2^-52 of its value: the angle, position times that, is then reduced exactly
+ * however far the position is.
  *   q: rows of q_heads x head_dim values, k and v of kv_heads x head_dim, FP32
  *      (the projections' outputs) or BF16 (GEMV_ROWS_*), row strides in
  *      elements; head_dim and rot_dim are even. Turned in FP32, rounded once.

@@ -29,12 +29,13 @@
 // warp-level MMAs: with 4 heads on a key-value head a byte of K or V takes 4
 // operations, and the tensor pipe is 13-23% busy while the HBM is the limit.
 //
-// What bounds it. Long lists the HBM: 64 x 32,768 tokens of 8 heads of 128
-// (BF16) 882 us, 7.3 TB/s, 1.08 of a copy's rate; FP8, 32 requests of up to
-// 16,384 85 us, 6.3 TB/s. Groups of 16 heads of 256 columns the warps'
-// instructions (64 us for 46 us of bytes). Short ones latency: 1 x 1,000
-// tokens 8.7 us, of which the launch, the lengths, the page numbers and the
-// first tokens follow each other for 5, and the pieces' join takes 3.
+// What bounds it. Long lists the HBM: 64 requests of 16,384 to 32,768 tokens of
+// 8 heads of 128 (BF16, 6.44 GB) 885 us, 7.3 TB/s, 1.07 of a copy's rate; FP8,
+// 32 requests of up to 16,384 85 us, 6.3 TB/s. Groups of 16 heads of 256
+// columns the warps' instructions (64 us for 46 us of bytes). Short ones
+// latency: 1 x 1,000 tokens 8.8 us, of which the launch, the lengths, the page
+// numbers and the first tokens follow each other for 5, and the pieces' join
+// takes 3.
 #pragma once
 
 #include <cstdint>
@@ -276,7 +277,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     const int qt = blockIdx.x - unit * p.qtiles;
     // CTAs work in teams of 2, 4 or 8 where the KV heads divide into such blocks: the list is one of head blocks, and
     // each CTA of a team takes its own head of the block. They read neighbouring memory at the same time, and the HBM
-    // gives more for it (FP8, 32 x 16,384 tokens: 220 -> 167 us; BF16, 64 x 32,768: 927 -> 884).
+    // gives more for it (FP8, 32 x 16,384 tokens: 220 -> 167 us; BF16, 64 x 16,384 to 32,768:
+    // 927 -> 884).
     const int blocks = p.kv_heads >> p.team_shift;
     const int cta = unit >> p.team_shift, member = unit & ((1 << p.team_shift) - 1);
     auto head_of = [&](int block) { return (block << p.team_shift) + member; };

@@ -15,7 +15,7 @@
 // against the blocks an SM holds. Measured (before the sines were laid out
 // without bank conflicts) with 1, 2, 4 and 8 tokens: 8,100 image patches of
 // 2 x 16 heads of 80 columns 22.1, 17.2, 18.0, 22.0 us, a prompt of 4,096
-// tokens of 48 FP32 heads 27.1, 23.0, 25.4, 30.8 us. Now 14.6 us (5.7 TB/s)
+// tokens of 48 FP32 heads 27.1, 23.0, 25.4, 30.8 us. Now 14.7 us (5.6 TB/s)
 // and 22.8 (6.6 TB/s).
 //
 // The angle is reduced exactly: freqs holds inv_freq / (2 pi) as a 64-bit
