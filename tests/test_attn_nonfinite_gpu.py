@@ -143,3 +143,20 @@ def test_no_weight_beside_values_that_are_not_finite(lens, value):
     seen = check(a)
     rows = sum(n > 0 for n in lens)
     assert seen["none"] == rows and seen["nan"] == (rows * (GROUP - 1) if math.isnan(value) else 0)
+
+
+@pytest.mark.parametrize("n", [40, 5000])
+def test_infinite_value_of_a_small_weight(n):
+    """Both parts of a weight are above zero down to 2^-110 of the largest, so its infinite v shows."""
+    drops = [3.0, 30.7, 60.3, 90.1, 100.9, 105.6, 108.2, 109.0]
+    a = make([n])
+    a.q.zero_()
+    for h, drop in enumerate(drops):
+        a.q[0, h * DIM] = -drop * math.log(2.0) / a.scale      # BF16: within 2^-8 of it, above 2^-110
+    for g in range(HEADS):
+        for j in range(n):
+            put(a, 0, 0, j, g, 0, 1.0 if j == n // 3 else 0.0)
+        put(a, 1, 0, n // 3, g, 5, math.inf)
+        put(a, 1, 0, n // 3, g, 6, -math.inf)
+    seen = check(a)
+    assert seen["inf"] == len(drops) and seen["nan"] == 0
