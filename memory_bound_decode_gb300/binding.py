@@ -453,7 +453,8 @@ def rope_args(*, q, k, q_out, positions, freqs, tokens: int, q_heads: int, kv_he
 
 def attn_args(*, q, out, lens, requests: int, q_heads: int, q_stride: int, out_stride: int, table, table_width: int,
               table_stride: int, scale: float, workspace, lse=None, token_start=None, status=None,
-              rows: int = 0, softcap: float = 0.0, window: int = 0, workspace_bytes: int | None = None) -> gemv_attn_args:
+              rows: int = 0, softcap: float = 0.0, window: int = 0,
+              workspace_bytes: int | None = None) -> gemv_attn_args:
     """``workspace_bytes``: the workspace's own size unless given; an address needs it."""
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None or isinstance(workspace, int) else workspace.nbytes
@@ -461,8 +462,8 @@ def attn_args(*, q, out, lens, requests: int, q_heads: int, q_stride: int, out_s
                    dict(q=q, out=out, lse=lse, lens=lens, token_start=token_start, status=status, table=table,
                         workspace=workspace),
                    dict(q_stride=q_stride, out_stride=out_stride, table_stride=table_stride, rows=rows,
-                        workspace_bytes=workspace_bytes, requests=requests, q_heads=q_heads, table_width=table_width, window=window, scale=scale,
-                        softcap=softcap))
+                        workspace_bytes=workspace_bytes, requests=requests, q_heads=q_heads, table_width=table_width,
+                        window=window, scale=scale, softcap=softcap))
 
 
 def gemv_block_tables(args: gemv_block_tables_args, stream=None, check: bool = True) -> int:

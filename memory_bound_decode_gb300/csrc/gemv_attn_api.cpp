@@ -119,8 +119,8 @@ int gemv_block_tables(const gemv_block_tables_args* a, void* stream) {
         return GEMV_ERR_INVALID;
     // More requests than 2^30 would carry the kernels' 32-bit counts of them past 2^31 (the middle of a search, the
     // next chunk's first).
-    if (a->requests < 1 || a->requests > (1 << 30) || a->page_size < 1 || a->num_pages < 1 || a->table_width < 1 || a->free_cap < 0 ||
-        (a->free_cap > 0 && !a->free_pages))
+    if (a->requests < 1 || a->requests > (1 << 30) || a->page_size < 1 || a->num_pages < 1 || a->table_width < 1 ||
+        a->free_cap < 0 || (a->free_cap > 0 && !a->free_pages))
         return GEMV_ERR_INVALID;
     if (static_cast<int64_t>(a->num_pages) * a->page_size > 0x7fffffffLL ||
         static_cast<int64_t>(a->table_width) * a->page_size > 0x7fffffffLL)
