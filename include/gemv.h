@@ -410,7 +410,8 @@ int gemv_workspace_release(void);
 /* GEMV_STATUS_BAD_PAGE: gemv_attn_decode met a page number outside the pool, a
  * length past its row of the table, or a query row out of range. Nothing is
  * read through it: those tokens count as masked, that length is cut, that
- * request is skipped. */
+ * request is skipped. gemv_cache_read met a token outside its request's row of
+ * the table or the pool: its rows are zeros. */
 #define GEMV_STATUS_BAD_PAGE 2u
 int gemv_device_status(unsigned int *bits, int reset);
 
@@ -525,7 +526,8 @@ int gemv_probe_sink_words(void);
  * and o_proj. gemv_block_tables gives every new token of a batch its page and
  * slot, gemv_rope_append turns q and k by their positions and writes k and v
  * into the paged cache at those slots, gemv_attn_decode attends from one new
- * token of each request to its pages. The rules above hold: asynchronous on
+ * token of each request to its pages, gemv_cache_read brings tokens of a cache
+ * back as rows. The rules above hold: asynchronous on
  * the stream, arguments checked before anything is launched, nothing
  * allocated, results the same from call to call. The calls run on the current
  * device, which must be the stream's and the tensors'. They may be captured;
@@ -548,10 +550,25 @@ int gemv_probe_sink_words(void);
  *   GEMV_CACHE_BF16: BF16 values; the scales are NULL.
  *   GEMV_CACHE_FP8:  E4M3 codes; a value is its code times k_scale[h] or
  *                    v_scale[h] (FP32, kv_heads each; NULL: 1).
+ *   GEMV_CACHE_FP8_BLOCK: E4M3 codes with a scale for each block of tokens and
+ *                    head, which gemv_rope_append finds as it writes. A block
+ *                    is block_tokens neighbouring slots of a page (1 to
+ *                    GEMV_MAX_BLOCK_TOKENS, a divisor of page_size); a value
+ *                    of slot s in page g is its code times
+ *                        k_block_scale[g * scale_page_stride +
+ *                            s / block_tokens * scale_block_stride +
+ *                            h * scale_head_stride]
+ *                    (v_block_scale for v; FP32; strides in elements, at least
+ *                    1 and at most 2^59, entries that do not overlap). k_scale
+ *                    and v_scale are NULL. Scales of visible tokens are
+ *                    positive normal numbers (0 counts as 2^-100). The other
+ *                    kinds do not read the fields from k_block_scale on.
  */
 #define GEMV_CACHE_BF16 0
 #define GEMV_CACHE_FP8 1
+#define GEMV_CACHE_FP8_BLOCK 3
 #define GEMV_MAX_HEAD_DIM 256
+#define GEMV_MAX_BLOCK_TOKENS 64
 
 typedef struct {
     void *k;
@@ -566,6 +583,12 @@ typedef struct {
     int32_t kv_heads;
     int32_t head_dim;
     int32_t kind;
+    float *k_block_scale;
+    float *v_block_scale;
+    int64_t scale_page_stride;
+    int64_t scale_block_stride;
+    int64_t scale_head_stride;
+    int32_t block_tokens;
 } gemv_kv_cache;
 
 /*
@@ -646,6 +669,17 @@ int gemv_block_tables(const gemv_block_tables_args *args, void *stream);
  * cache is written. Slots that are in the pool must differ from each other.
  * FP8: the code nearest to value / scale, at most 448 in magnitude (infinities
  * too; NaN stays NaN).
+ * GEMV_CACHE_FP8_BLOCK: the tokens that a call writes into a block are
+ * neighbours in the batch, in the order of their slots and without gaps, as
+ * gemv_block_tables numbers them (else that block's scales and codes are
+ * undefined). With a the largest magnitude among the finite values of a head's
+ * new rows of the block, need = max(2^-30, the smallest power of two that is
+ * at least a / 448). Where the first of them takes the block's first slot, the
+ * scale becomes need. Else the block holds earlier tokens: the scale becomes
+ * max(scale, need), and where it grows the codes of the slots before the first
+ * new one become the codes nearest to code * old scale / new scale (between
+ * powers of two exactly the same values, but for those that fall among E4M3's
+ * subnormals). A repeated call leaves the same bits.
  */
 #define GEMV_ROWS_F32 0
 #define GEMV_ROWS_BF16 1
@@ -688,6 +722,39 @@ int gemv_rope_append(const gemv_rope_args *args, const gemv_kv_cache *cache, voi
 int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
 
 /*
+ * Tokens of a cache back as rows, for the next piece of a prompt, say: row i of
+ * k_out and v_out, row_start[r] <= i < row_start[r + 1], becomes k and v of
+ * token begin[r] + i - row_start[r] of request r, whose pages are
+ * table[r * table_stride + b]: a value of the cache (for FP8 code times scale),
+ * rounded once to the rows' type (row_type: GEMV_ROWS_*).
+ *   k_out, v_out: rows of kv_heads x head_dim values, strides in elements
+ *           (multiples of 16 bytes), 16-byte aligned; one of them may be NULL.
+ *   begin:  requests entries, or NULL: every request from its token 0.
+ *   row_start: requests + 1 entries, ascending from 0 on. Rows from
+ *           row_start[requests] on stay as they were; none past `rows` (what
+ *           k_out and v_out hold) is written.
+ * A token before 0, past its request's row of the table, or in a page outside
+ * the pool reads as zeros and sets GEMV_STATUS_BAD_PAGE. requests = 0 and
+ * rows = 0 are allowed and do nothing.
+ */
+typedef struct {
+    const int32_t *table;
+    const int32_t *begin;
+    const int32_t *row_start;
+    void *k_out;
+    void *v_out;
+    int64_t table_stride;
+    int64_t k_out_stride;
+    int64_t v_out_stride;
+    int64_t rows;
+    int32_t requests;
+    int32_t table_width;
+    int32_t row_type;
+} gemv_cache_read_args;
+
+int gemv_cache_read(const gemv_cache_read_args *args, const gemv_kv_cache *cache, void *stream);
+
+/*
  * Attention of one new token per request over its pages: with j over the
  * visible tokens of request r,
  *     s_j = scale * q . k_j           (softcap > 0: softcap * tanh(s_j / softcap))
@@ -727,7 +794,9 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * Products of BF16 (FP8: codes widened exactly to FP16, and q scaled into FP16
  * by a power of two per head) are summed in FP32, the softmax is kept in FP32;
  * the probabilities, relative to the largest, meet V as two BF16 parts (2^-16;
- * FP8: as FP16, with 11 bits down to 2^-29 of the largest). requests = 0 is
+ * FP8: as FP16, with 11 bits down to 2^-29 of the largest; with a scale for each
+ * block the probabilities times v's scales, relative to the largest of those;
+ * what is below 2^-126 of it counts as 0). requests = 0 is
  * allowed and does nothing. GEMV_ERR_UNSUPPORTED: more than 1,024 query heads
  * per key-value head; requests * kv_heads * (table_width * page_size / 16 + 2)
  * above 2,130,706,432.

@@ -49,6 +49,7 @@ EXPORTED = [
     "gemv_w4_bf16", "gemv_w4_query_launch", "gemv_fp8_bf16", "gemv_fp8_query_launch",
     "gemv_probe_stream_read", "gemv_probe_sink_words",
     "gemv_block_tables", "gemv_rope", "gemv_rope_append", "gemv_rope_freqs", "gemv_attn_decode", "gemv_attn_query",
+    "gemv_cache_read",
     "gemv_status_string", "gemv_last_cuda_error",
 ]
 
@@ -87,7 +88,9 @@ class gemv_launch_info(ctypes.Structure):
 
 GEMV_CACHE_BF16 = 0
 GEMV_CACHE_FP8 = 1
+GEMV_CACHE_FP8_BLOCK = 3
 GEMV_MAX_HEAD_DIM = 256
+GEMV_MAX_BLOCK_TOKENS = 64
 GEMV_ROWS_F32 = 0
 GEMV_ROWS_BF16 = 1
 GEMV_PAIRS_HALF = 0
@@ -100,7 +103,10 @@ i32 = ctypes.c_int32
 class gemv_kv_cache(ctypes.Structure):
     _fields_ = ([(n, vp) for n in ("k", "v")] + [(n, i64) for n in ("page_stride", "head_stride", "slot_stride")]
                 + [(n, vp) for n in ("k_scale", "v_scale")]
-                + [(n, i32) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "kind")])
+                + [(n, i32) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "kind")]
+                + [(n, vp) for n in ("k_block_scale", "v_block_scale")]
+                + [(n, i64) for n in ("scale_page_stride", "scale_block_stride", "scale_head_stride")]
+                + [("block_tokens", i32)])
 
 
 class gemv_block_tables_args(ctypes.Structure):
@@ -123,6 +129,12 @@ class gemv_attn_args(ctypes.Structure):
                 + [(n, i64) for n in ("q_stride", "out_stride", "table_stride", "rows", "workspace_bytes")]
                 + [(n, i32) for n in ("requests", "q_heads", "table_width", "window")]
                 + [("scale", ctypes.c_float), ("softcap", ctypes.c_float)])
+
+
+class gemv_cache_read_args(ctypes.Structure):
+    _fields_ = ([(n, vp) for n in ("table", "begin", "row_start", "k_out", "v_out")]
+                + [(n, i64) for n in ("table_stride", "k_out_stride", "v_out_stride", "rows")]
+                + [(n, i32) for n in ("requests", "table_width", "row_type")])
 
 
 class gemv_attn_info(ctypes.Structure):
@@ -221,6 +233,7 @@ def _load(path: str) -> ctypes.CDLL:
     L.gemv_rope_append.argtypes = [ctypes.POINTER(gemv_rope_args), ctypes.POINTER(gemv_kv_cache), vp]
     L.gemv_rope_freqs.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.c_int, ctypes.POINTER(i64)]
     L.gemv_attn_decode.argtypes = [ctypes.POINTER(gemv_attn_args), ctypes.POINTER(gemv_kv_cache), vp]
+    L.gemv_cache_read.argtypes = [ctypes.POINTER(gemv_cache_read_args), ctypes.POINTER(gemv_kv_cache), vp]
     L.gemv_attn_query.argtypes = [ctypes.c_int] * 5 + [ctypes.POINTER(gemv_attn_info)]
     L.gemv_status_string.argtypes = [ctypes.c_int]
     L.gemv_status_string.restype = ctypes.c_char_p
@@ -421,10 +434,14 @@ def _record(cls, pointers: dict, numbers: dict):
 
 def kv_cache(k, v, *, num_pages: int, page_size: int, kv_heads: int, head_dim: int, page_stride: int,
              head_stride: int, slot_stride: int, kind: int = GEMV_CACHE_BF16, k_scale=None,
-             v_scale=None) -> gemv_kv_cache:
-    """A paged cache (see gemv.h); strides in elements."""
-    return _record(gemv_kv_cache, dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale),
-                   dict(num_pages=num_pages, page_size=page_size, kv_heads=kv_heads, head_dim=head_dim,
+             v_scale=None, k_block_scale=None, v_block_scale=None, block_tokens: int = 0, scale_page_stride: int = 0,
+             scale_block_stride: int = 0, scale_head_stride: int = 0) -> gemv_kv_cache:
+    """A paged cache (see gemv.h); strides in elements. From k_block_scale on: GEMV_CACHE_FP8_BLOCK."""
+    return _record(gemv_kv_cache, dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, k_block_scale=k_block_scale,
+                                       v_block_scale=v_block_scale),
+                   dict(block_tokens=block_tokens, scale_page_stride=scale_page_stride,
+                        scale_block_stride=scale_block_stride, scale_head_stride=scale_head_stride,
+                        num_pages=num_pages, page_size=page_size, kv_heads=kv_heads, head_dim=head_dim,
                         page_stride=page_stride, head_stride=head_stride, slot_stride=slot_stride, kind=kind))
 
 
@@ -466,6 +483,15 @@ def attn_args(*, q, out, lens, requests: int, q_heads: int, q_stride: int, out_s
                         window=window, scale=scale, softcap=softcap))
 
 
+def cache_read_args(*, table, table_width: int, table_stride: int, row_start, requests: int, rows: int, begin=None,
+                    k_out=None, v_out=None, k_out_stride: int = 0, v_out_stride: int = 0,
+                    row_type: int = GEMV_ROWS_BF16) -> gemv_cache_read_args:
+    return _record(gemv_cache_read_args,
+                   dict(table=table, begin=begin, row_start=row_start, k_out=k_out, v_out=v_out),
+                   dict(table_stride=table_stride, k_out_stride=k_out_stride, v_out_stride=v_out_stride, rows=rows,
+                        requests=requests, table_width=table_width, row_type=row_type))
+
+
 def gemv_block_tables(args: gemv_block_tables_args, stream=None, check: bool = True) -> int:
     """Pages, slots and positions of a step's new tokens (see gemv.h)."""
     rc = lib().gemv_block_tables(ctypes.byref(args), _stream(stream))
@@ -505,6 +531,12 @@ def gemv_attn_decode(args: gemv_attn_args, cache: gemv_kv_cache, stream=None, ch
     """Attention of one new token per request over its pages (see gemv.h)."""
     rc = lib().gemv_attn_decode(ctypes.byref(args), ctypes.byref(cache), _stream(stream))
     return _check(rc, "gemv_attn_decode") if check else rc
+
+
+def gemv_cache_read(args: gemv_cache_read_args, cache: gemv_kv_cache, stream=None, check: bool = True) -> int:
+    """Tokens of a cache back as rows (see gemv.h)."""
+    rc = lib().gemv_cache_read(ctypes.byref(args), ctypes.byref(cache), _stream(stream))
+    return _check(rc, "gemv_cache_read") if check else rc
 
 
 def gemv_attn_query(q_heads: int, kv_heads: int, head_dim: int, kind: int, sm_count: int) -> dict:

@@ -40,8 +40,13 @@ SOURCES = [
     "gemv_attn_fp8_64.cu",
     "gemv_attn_fp8_128.cu",
     "gemv_attn_fp8_256.cu",
+    "gemv_attn_fp8b_64.cu",
+    "gemv_attn_fp8b_128.cu",
+    "gemv_attn_fp8b_256.cu",
     "gemv_attn_dispatch.cu",
     "gemv_rope.cu",
+    "gemv_append_blocks.cu",
+    "gemv_cache_read.cu",
     "gemv_blocks.cu",
     "planner.cpp",
     "gemv_api.cpp",
@@ -50,7 +55,7 @@ SOURCES = [
 HEADERS = ["gemv_internal.h", "gemv_common.cuh", "gemv_kernel.cuh", "gemv_mma_kernel.cuh", "gemv_w4_kernel.cuh",
            "gemv_tc_kernel.cuh",
            "gemv_streamk_kernel.cuh", "gemv_fp8_kernel.cuh", "gemv_attn_internal.h", "gemv_attn_kernel.cuh",
-           "gemv_attn_instances.cuh", os.path.join("..", "..", "include", "gemv.h")]
+           "gemv_attn_instances.cuh", "gemv_rows.cuh", os.path.join("..", "..", "include", "gemv.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

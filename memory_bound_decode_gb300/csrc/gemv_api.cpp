@@ -1193,15 +1193,16 @@ int gemv_device_status(unsigned int* bits, int reset) {
     if (!bits) return GEMV_ERR_INVALID;
     *bits = 0;
     // Each kernel translation unit keeps its own status word.
-    unsigned int b1 = 0, b2 = 0, b3 = 0, b4 = 0, b5 = 0, b6 = 0;
+    unsigned int b1 = 0, b2 = 0, b3 = 0, b4 = 0, b5 = 0, b6 = 0, b7 = 0;
     cudaError_t e = gemv::read_fma_status(&b1, reset != 0);
     if (e == cudaSuccess) e = gemv::read_mma_status_nb1(&b2, reset != 0);
     if (e == cudaSuccess) e = gemv::read_mma_status_nb2(&b3, reset != 0);
     if (e == cudaSuccess) e = gemv::read_fp8_status(&b4, reset != 0);
     if (e == cudaSuccess) e = gemv::read_tc_status(&b5, reset != 0);
     if (e == cudaSuccess && attn_in_use()) e = gemv::read_attn_status(&b6, reset != 0);
+    if (e == cudaSuccess) e = gemv::read_read_status(&b7, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e);
-    *bits = b1 | b2 | b3 | b4 | b5 | b6;
+    *bits = b1 | b2 | b3 | b4 | b5 | b6 | b7;
     return GEMV_OK;
 }
 

@@ -1,6 +1,6 @@
 // C-ABI front end of the decode step's attention half: argument checks and
-// launches of the block tables, the rotary positions with the cache write, and
-// the paged decode attention.
+// launches of the block tables, the rotary positions with the cache write, the
+// paged decode attention, and the cache read back as rows.
 #include <cmath>
 #include <cstdint>
 
@@ -17,12 +17,31 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // that the kernels' 64-bit offsets cannot wrap.
 bool fits(int64_t n, int64_t stride) { return n <= 1 || stride <= (int64_t(1) << 60) / n; }
 
+bool known_kind(int kind) {
+    return kind == GEMV_CACHE_BF16 || kind == GEMV_CACHE_FP8 || kind == GEMV_CACHE_FP8_BLOCK;
+}
+// Elements of a 16-byte access.
+int unit_of(int kind) { return kind == GEMV_CACHE_BF16 ? 8 : 16; }
+
+// The fields of a cache with a scale for each block.
+int check_block_scales(const gemv_kv_cache* c) {
+    if (!c->k_block_scale || !c->v_block_scale || c->k_scale || c->v_scale) return GEMV_ERR_INVALID;
+    if (c->block_tokens < 1 || c->block_tokens > GEMV_MAX_BLOCK_TOKENS || c->page_size % c->block_tokens != 0)
+        return GEMV_ERR_INVALID;
+    const int64_t n[3] = {c->num_pages, c->page_size / c->block_tokens, c->kv_heads};
+    const int64_t st[3] = {c->scale_page_stride, c->scale_block_stride, c->scale_head_stride};
+    for (int i = 0; i < 3; ++i)
+        if (st[i] < (n[i] > 1) || st[i] > (int64_t(1) << 59) || !fits(n[i], 4 * st[i])) return GEMV_ERR_INVALID;
+    if (!aligned(c->k_block_scale, 4) || !aligned(c->v_block_scale, 4)) return GEMV_ERR_ALIGN;
+    return GEMV_OK;
+}
+
 int check_cache(const gemv_kv_cache* c) {
     if (!c || !c->k || !c->v) return GEMV_ERR_INVALID;
-    if (c->kind != GEMV_CACHE_BF16 && c->kind != GEMV_CACHE_FP8) return GEMV_ERR_INVALID;
+    if (!known_kind(c->kind)) return GEMV_ERR_INVALID;
     if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->kv_heads > 4096) return GEMV_ERR_INVALID;
     if (static_cast<int64_t>(c->num_pages) * c->page_size > 0x7fffffffLL) return GEMV_ERR_INVALID;
-    const int unit = c->kind == GEMV_CACHE_FP8 ? 16 : 8;      // elements of a 16-byte access
+    const int unit = unit_of(c->kind);
     if (c->head_dim < unit || c->head_dim > GEMV_MAX_HEAD_DIM || c->head_dim % unit != 0) return GEMV_ERR_INVALID;
     const int64_t d = c->head_dim;
     const int64_t most = int64_t(1) << 59;                     // so that no product below can wrap
@@ -37,7 +56,7 @@ int check_cache(const gemv_kv_cache* c) {
     if (c->page_stride % unit != 0 || c->head_stride % unit != 0 || c->slot_stride % unit != 0 || !aligned(c->k, 16) ||
         !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
         return GEMV_ERR_ALIGN;
-    return GEMV_OK;
+    return c->kind == GEMV_CACHE_FP8_BLOCK ? check_block_scales(c) : GEMV_OK;
 }
 
 // log2 of a power of two, -1 of other sizes.
@@ -48,7 +67,7 @@ int shift_of(int32_t n) {
     return s;
 }
 
-int elem_bytes(const gemv_kv_cache* c) { return c->kind == GEMV_CACHE_FP8 ? 1 : 2; }
+int elem_bytes(const gemv_kv_cache* c) { return c->kind == GEMV_CACHE_BF16 ? 2 : 1; }
 
 int check_rope(const gemv_rope_args* a) {
     if (!a || !a->q || !a->k || !a->q_out || !a->positions || !a->freqs) return GEMV_ERR_INVALID;
@@ -219,18 +238,24 @@ int gemv_rope_append(const gemv_rope_args* a, const gemv_kv_cache* c, void* stre
     p.head_stride = c->head_stride * es;
     p.slot_stride = c->slot_stride * es;
     p.num_slots = static_cast<int64_t>(c->num_pages) * c->page_size;
+    if (c->kind == GEMV_CACHE_FP8_BLOCK) {
+        const gemv::BlockScales b = {c->k_block_scale, c->v_block_scale, c->scale_page_stride, c->scale_block_stride,
+                                     c->scale_head_stride, c->block_tokens, shift_of(c->block_tokens)};
+        return finish(gemv::launch_append_blocks(p, b, sm_count, static_cast<cudaStream_t>(stream),
+                                                 gemv::api_pdl_enabled()));
+    }
     return finish(gemv::launch_rope(p, sm_count, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
 }
 
 int gemv_attn_query(int q_heads, int kv_heads, int head_dim, int kind, int sm_count, gemv_attn_info* out) {
     if (!out || sm_count < 1 || kv_heads < 1 || kv_heads > 4096 || q_heads < kv_heads || q_heads % kv_heads != 0)
         return GEMV_ERR_INVALID;
-    if (kind != GEMV_CACHE_BF16 && kind != GEMV_CACHE_FP8) return GEMV_ERR_INVALID;
-    const int unit = kind == GEMV_CACHE_FP8 ? 16 : 8;
+    if (!known_kind(kind)) return GEMV_ERR_INVALID;
+    const int unit = unit_of(kind);
     if (head_dim < unit || head_dim > GEMV_MAX_HEAD_DIM || head_dim % unit != 0) return GEMV_ERR_INVALID;
     if (q_heads / kv_heads > gemv::kAttnMaxGroup) return GEMV_ERR_UNSUPPORTED;
     gemv::AttnLaunch l = {};
-    const int rc = gemv::plan_attn(q_heads, kv_heads, head_dim, kind == GEMV_CACHE_FP8, sm_count, &l);
+    const int rc = gemv::plan_attn(q_heads, kv_heads, head_dim, kind, sm_count, &l);
     if (rc != GEMV_OK) return rc;
     out->workspace_bytes = l.workspace_bytes;
     out->grid = l.grid;
@@ -271,13 +296,12 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
         return GEMV_ERR_UNSUPPORTED;
     if (a->requests == 0) return GEMV_OK;
     gemv::AttnLaunch l = {};
-    const int fp8 = c->kind == GEMV_CACHE_FP8;
     // What a GPU of one SM needs, so that a size left out is refused where there is none; then what this one needs.
-    if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, fp8, 1, &l)) != GEMV_OK) return rc;
+    if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, c->kind, 1, &l)) != GEMV_OK) return rc;
     if (a->workspace_bytes < l.workspace_bytes) return GEMV_ERR_INVALID;
     int sm_count = 0;
     if ((rc = gemv::api_attn_state(&sm_count)) != GEMV_OK) return rc;
-    if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, fp8, sm_count, &l)) != GEMV_OK) return rc;
+    if ((rc = gemv::plan_attn(a->q_heads, c->kv_heads, c->head_dim, c->kind, sm_count, &l)) != GEMV_OK) return rc;
     if (a->workspace_bytes < l.workspace_bytes) return GEMV_ERR_INVALID;
     gemv::AttnParams p = {};
     p.q = static_cast<const uint16_t*>(a->q);
@@ -332,13 +356,85 @@ int gemv_attn_decode(const gemv_attn_args* a, const gemv_kv_cache* c, void* stre
                                c->kv_heads > 1 ? p.head_stride : c->head_dim * es,
                                c->num_pages > 1 ? p.page_stride : c->head_dim * es};
         const int line = l.dt * es < 128 ? l.dt : static_cast<int>(128 / es);
-        p.tma = gemv::api_encode_pool(&p.kmap, c->k, fp8, dims, st, line, rows) &&
-                gemv::api_encode_pool(&p.vmap, c->v, fp8, dims, st, line, rows);
+        p.tma = gemv::api_encode_pool(&p.kmap, c->k, es == 1, dims, st, line, rows) &&
+                gemv::api_encode_pool(&p.vmap, c->v, es == 1, dims, st, line, rows);
         p.box_shift = shift_of(rows);
+    }
+    if (c->kind == GEMV_CACHE_FP8_BLOCK) {
+        p.k_block_scale = c->k_block_scale;
+        p.v_block_scale = c->v_block_scale;
+        p.scale_page_stride = c->scale_page_stride;
+        p.scale_block_stride = c->scale_block_stride;
+        p.scale_head_stride = c->scale_head_stride;
+        p.block_tokens = c->block_tokens;
+        p.block_shift = shift_of(c->block_tokens);
     }
     p.scale = a->scale;
     p.softcap = a->softcap;
     return finish(gemv::launch_attn(p, l, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
+}
+
+int gemv_cache_read(const gemv_cache_read_args* a, const gemv_kv_cache* c, void* stream) {
+    if (!a || !a->table || !a->row_start || (!a->k_out && !a->v_out)) return GEMV_ERR_INVALID;
+    int rc = check_cache(c);
+    if (rc != GEMV_OK) return rc;
+    if (a->row_type != GEMV_ROWS_F32 && a->row_type != GEMV_ROWS_BF16) return GEMV_ERR_INVALID;
+    if (a->requests < 0 || a->requests > (1 << 30) || a->rows < 0 || a->rows > 0x7fffffffLL) return GEMV_ERR_INVALID;
+    const int64_t width = static_cast<int64_t>(c->kv_heads) * c->head_dim, most = int64_t(1) << 31;
+    if (a->table_width < 1 || a->table_stride < a->table_width || a->table_stride > most) return GEMV_ERR_INVALID;
+    if (static_cast<int64_t>(a->table_width) * c->page_size > 0x7fffffffLL) return GEMV_ERR_INVALID;
+    if ((a->k_out && (a->k_out_stride < width || a->k_out_stride > most)) ||
+        (a->v_out && (a->v_out_stride < width || a->v_out_stride > most)))
+        return GEMV_ERR_INVALID;
+    const int es = a->row_type == GEMV_ROWS_F32 ? 4 : 2, unit = 16 / es;
+    if ((a->k_out && a->k_out_stride % unit != 0) || (a->v_out && a->v_out_stride % unit != 0) ||
+        !aligned(a->k_out, 16) || !aligned(a->v_out, 16) || !aligned(a->table, 4) || !aligned(a->begin, 4) ||
+        !aligned(a->row_start, 4))
+        return GEMV_ERR_ALIGN;
+    if (a->requests == 0 || a->rows == 0) return GEMV_OK;
+    int sm_count = 0;
+    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
+    gemv::ReadParams p = {};
+    p.pool[0] = static_cast<const unsigned char*>(c->k);
+    p.pool[1] = static_cast<const unsigned char*>(c->v);
+    p.out[0] = static_cast<unsigned char*>(a->k_out);
+    p.out[1] = static_cast<unsigned char*>(a->v_out);
+    p.out_stride[0] = a->k_out_stride * es;
+    p.out_stride[1] = a->v_out_stride * es;
+    p.table = a->table;
+    p.begin = a->begin;
+    p.row_start = a->row_start;
+    p.table_stride = a->table_stride;
+    p.page_stride = c->page_stride * elem_bytes(c);
+    p.head_stride = c->head_stride * elem_bytes(c);
+    p.slot_stride = c->slot_stride * elem_bytes(c);
+    p.rows = a->rows;
+    p.requests = a->requests;
+    p.table_width = a->table_width;
+    p.num_pages = c->num_pages;
+    p.page_size = c->page_size;
+    p.page_shift = shift_of(c->page_size);
+    p.kv_heads = c->kv_heads;
+    p.head_dim = c->head_dim;
+    p.fp8 = c->kind != GEMV_CACHE_BF16;
+    p.rows_f32 = a->row_type == GEMV_ROWS_F32;
+    // A scale per head is one for blocks of a page, the same in every page.
+    p.block_tokens = c->page_size;
+    p.block_shift = p.page_shift;
+    if (c->kind == GEMV_CACHE_FP8_BLOCK) {
+        p.scale[0] = c->k_block_scale;
+        p.scale[1] = c->v_block_scale;
+        p.scale_page_stride = c->scale_page_stride;
+        p.scale_block_stride = c->scale_block_stride;
+        p.scale_head_stride = c->scale_head_stride;
+        p.block_tokens = c->block_tokens;
+        p.block_shift = shift_of(c->block_tokens);
+    } else {
+        p.scale[0] = c->k_scale;
+        p.scale[1] = c->v_scale;
+        p.scale_head_stride = 1;
+    }
+    return finish(gemv::launch_read(p, static_cast<cudaStream_t>(stream), gemv::api_pdl_enabled()));
 }
 
 }  // extern "C"

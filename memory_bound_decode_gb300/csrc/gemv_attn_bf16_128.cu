@@ -2,5 +2,5 @@
 #include "gemv_attn_instances.cuh"
 
 namespace gemv {
-GEMV_ATTN_UNIT(bf16_128, 128, false, 4)
+GEMV_ATTN_UNIT(bf16_128, 128, false, false, 4)
 }  // namespace gemv

@@ -2,5 +2,5 @@
 #include "gemv_attn_instances.cuh"
 
 namespace gemv {
-GEMV_ATTN_UNIT(bf16_256, 256, false, 2)
+GEMV_ATTN_UNIT(bf16_256, 256, false, false, 2)
 }  // namespace gemv

@@ -2,5 +2,5 @@
 #include "gemv_attn_instances.cuh"
 
 namespace gemv {
-GEMV_ATTN_UNIT(bf16_64, 64, false, 4)
+GEMV_ATTN_UNIT(bf16_64, 64, false, false, 4)
 }  // namespace gemv

@@ -16,6 +16,9 @@ GEMV_ATTN_DECL(bf16_256)
 GEMV_ATTN_DECL(fp8_64)
 GEMV_ATTN_DECL(fp8_128)
 GEMV_ATTN_DECL(fp8_256)
+GEMV_ATTN_DECL(fp8b_64)
+GEMV_ATTN_DECL(fp8b_128)
+GEMV_ATTN_DECL(fp8b_256)
 
 // The instance of a shape: the smallest head size that holds head_dim, and as
 // many blocks of 8 query heads as the group needs, up to what the output
@@ -23,9 +26,10 @@ GEMV_ATTN_DECL(fp8_256)
 // columns). A larger group is cut into tiles, one per CTA of a set of CTAs
 // that read the same tokens at the same time. CTAs also form teams of 2, 4 or
 // 8, as far as both the KV heads and the CTAs divide, a head of a block each.
-int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, AttnLaunch* l) {
+int plan_attn(int q_heads, int kv_heads, int head_dim, int kind, int sm_count, AttnLaunch* l) {
     const int group = q_heads / kv_heads;
-    l->fp8 = fp8;
+    l->fp8 = kind != GEMV_CACHE_BF16;
+    l->block = kind == GEMV_CACHE_FP8_BLOCK;
     l->dt = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     const int most = l->dt == 256 ? 2 : 4;
     const int blocks = (group + 7) / 8;
@@ -38,11 +42,16 @@ int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, At
     const int64_t heads = static_cast<int64_t>(l->grid) * (2 + kAttnWarps) * l->nb * 8;   // pieces of CTAs and warps
     l->workspace_bytes = kAttnTickets * 4 + heads * (2 + l->dt) * 4;
     l->warps = kAttnWarps;
-    l->slice = attn_slice(l->dt, l->nb, fp8 != 0, true);
+    l->slice = attn_slice(l->dt, l->nb, l->fp8 != 0, true);
     return GEMV_OK;
 }
 
 cudaError_t launch_attn(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl) {
+    if (l.block) {
+        if (l.dt == 64) return attn_launch_fp8b_64(p, l, s, pdl);
+        if (l.dt == 128) return attn_launch_fp8b_128(p, l, s, pdl);
+        return attn_launch_fp8b_256(p, l, s, pdl);
+    }
     if (l.fp8) {
         if (l.dt == 64) return attn_launch_fp8_64(p, l, s, pdl);
         if (l.dt == 128) return attn_launch_fp8_128(p, l, s, pdl);
@@ -55,7 +64,8 @@ cudaError_t launch_attn(const AttnParams& p, const AttnLaunch& l, cudaStream_t s
 
 cudaError_t prepare_attn() {
     cudaError_t (*const all[])() = {attn_prepare_bf16_64, attn_prepare_bf16_128, attn_prepare_bf16_256,
-                                    attn_prepare_fp8_64, attn_prepare_fp8_128, attn_prepare_fp8_256};
+                                    attn_prepare_fp8_64, attn_prepare_fp8_128, attn_prepare_fp8_256,
+                                    attn_prepare_fp8b_64, attn_prepare_fp8b_128, attn_prepare_fp8b_256};
     for (auto f : all) {
         const cudaError_t e = f();
         if (e != cudaSuccess) return e;
@@ -66,7 +76,9 @@ cudaError_t prepare_attn() {
 cudaError_t read_attn_status(unsigned int* bits, bool reset) {
     cudaError_t (*const all[])(unsigned int*, bool) = {attn_status_bf16_64, attn_status_bf16_128,
                                                        attn_status_bf16_256, attn_status_fp8_64,
-                                                       attn_status_fp8_128, attn_status_fp8_256};
+                                                       attn_status_fp8_128, attn_status_fp8_256,
+                                                       attn_status_fp8b_64, attn_status_fp8b_128,
+                                                       attn_status_fp8b_256};
     *bits = 0;
     for (auto f : all) {
         unsigned int b = 0;

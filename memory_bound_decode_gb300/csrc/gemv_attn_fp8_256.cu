@@ -2,5 +2,5 @@
 #include "gemv_attn_instances.cuh"
 
 namespace gemv {
-GEMV_ATTN_UNIT(fp8_256, 256, true, 2)
+GEMV_ATTN_UNIT(fp8_256, 256, true, false, 2)
 }  // namespace gemv

@@ -2,5 +2,5 @@
 #include "gemv_attn_instances.cuh"
 
 namespace gemv {
-GEMV_ATTN_UNIT(fp8_64, 64, true, 4)
+GEMV_ATTN_UNIT(fp8_64, 64, true, false, 4)
 }  // namespace gemv

@@ -58,6 +58,8 @@ struct AttnParams {
     const unsigned char* vc;
     const float* k_scale;
     const float* v_scale;
+    const float* k_block_scale; // a scale per block of tokens and head
+    const float* v_block_scale;
     float* part;                // two pieces per CTA, of rows cut between CTAs: outputs,
     float* part_ml;             // maxima and sums
     float* part_warp;           // a piece per warp, of rows cut between a CTA's warps
@@ -65,10 +67,12 @@ struct AttnParams {
     int64_t q_stride, out_stride, table_stride;
     int64_t table_entries;      // from the table's first to its last
     int64_t page_stride, head_stride, slot_stride;   // bytes
+    int64_t scale_page_stride, scale_block_stride, scale_head_stride;   // elements
     int64_t rows;               // rows of q and out
     int32_t requests, q_heads, kv_heads, group, qtiles, team_shift;
     int32_t head_dim, page_size, num_pages, window, max_len;
     int32_t page_shift;         // log2 of page_size, -1 if it is no power of two
+    int32_t block_tokens, block_shift;               // the same of a block with a scale
     int32_t tma;                // 1: tensor copies of 1 << box_shift slots
     int32_t box_shift;
     uint32_t quarter_of;        // x * quarter_of >> 20 is x / (head_dim / 4), up to 2,048
@@ -81,13 +85,14 @@ struct AttnLaunch {
     int dt;            // head size the instance is built for: 64, 128 or 256
     int nb;            // blocks of 8 query heads a CTA carries
     int fp8;
+    int block;         // a scale for each block of tokens and head
     int warps;
     int slice;         // tokens a warp takes at a time
     int qtiles, team_shift, grid;
     int64_t workspace_bytes;
 };
 
-int plan_attn(int q_heads, int kv_heads, int head_dim, int fp8, int sm_count, AttnLaunch* l);
+int plan_attn(int q_heads, int kv_heads, int head_dim, int kind, int sm_count, AttnLaunch* l);   // kind: GEMV_CACHE_*
 
 cudaError_t launch_attn(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl);
 cudaError_t prepare_attn();
@@ -118,6 +123,39 @@ struct RopeParams {
 };
 
 cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t s, bool pdl);
+
+// The write into a cache with a scale for each block of tokens and head.
+struct BlockScales {
+    float* k;
+    float* v;
+    int64_t page_stride, block_stride, head_stride;       // elements
+    int32_t tokens;             // of a block
+    int32_t shift;              // its log2, -1 if it is no power of two
+};
+
+cudaError_t launch_append_blocks(const RopeParams& p, const BlockScales& b, int sm_count, cudaStream_t s, bool pdl);
+
+// ---- rows read back from a cache --------------------------------------------------
+
+struct ReadParams {
+    const unsigned char* pool[2];                         // k, v
+    unsigned char* out[2];                                // null: not wanted
+    const float* scale[2];      // per head, or of BlockScales' layout
+    const int32_t* table;
+    const int32_t* begin;       // null: 0
+    const int32_t* row_start;
+    int64_t table_stride;
+    int64_t out_stride[2];                                // bytes
+    int64_t page_stride, head_stride, slot_stride;        // bytes
+    int64_t scale_page_stride, scale_block_stride, scale_head_stride;
+    int64_t rows;
+    int32_t requests, table_width, num_pages, page_size, kv_heads, head_dim;
+    int32_t page_shift, block_tokens, block_shift;
+    int32_t fp8, rows_f32;
+};
+
+cudaError_t launch_read(const ReadParams& p, cudaStream_t s, bool pdl);
+cudaError_t read_read_status(unsigned int* bits, bool reset);
 
 // ---- block tables ---------------------------------------------------------------
 

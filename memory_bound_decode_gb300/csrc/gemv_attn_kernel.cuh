@@ -19,6 +19,17 @@
 // workspace. Pieces (FP32 output, maximum, sum) are always joined in list
 // order, so the result does not depend on which CTA that is.
 //
+// Scales. An FP8 cache with one scale per head has it in q and in the output's
+// factor. With a scale ks, vs for each block of tokens, a score is multiplied by
+// its token's ks, and with M the running maximum of s_j + log vs_j
+//
+//   w_j = exp(s_j + log vs_j - M),  out = sum_j w_j code_j / sum_j (w_j / vs_j):
+//
+// one exponential and one maximum as before, and the weights, which meet the
+// codes in FP16, are relative to the largest of the products that are summed,
+// however far the scales of the blocks are apart. The scales of a slice's tokens
+// come by asynchronous copies beside its K, counted on the same barrier.
+//
 // Tiles. The group of query heads that share a key-value head are the narrow
 // side (N = 8) of the MMAs, 16 tokens of a slice (scores) or 16 columns of
 // the head (output) the wide one: S^T = K Q^T and O^T = V^T P^T. K and V then
@@ -71,6 +82,9 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_or_zero(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
 }
 // This thread's arrival at the barrier, once its copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
@@ -155,6 +169,12 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     return r;
 }
 
+__device__ __forceinline__ float log2_ftz(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -211,9 +231,11 @@ __device__ __forceinline__ int attn_slices(const AttnParams& p, int len) {
 }
 
 // DT: head size of the instance (head_dim <= DT; columns past head_dim are
-// zero). NB: blocks of 8 query heads.
-template <int DT, int NB, bool FP8, bool TMA>
+// zero). NB: blocks of 8 query heads. BLOCK: FP8 with a scale for each block of
+// tokens and head.
+template <int DT, int NB, bool FP8, bool TMA, bool BLOCK = false>
 struct AttnShape {
+    static_assert(FP8 || !BLOCK, "codes have scales");
     static constexpr int kWarps = kAttnWarps;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kSlice = attn_slice(DT, NB, FP8, TMA);
@@ -232,15 +254,21 @@ struct AttnShape {
     static constexpr int kRaw = NB * 8 * kRawStride;
     // A warp's first piece waits in shared memory for the others where there is room, else in the workspace.
     static constexpr int kFirst = NB * 8 * DT * 4;
-    static constexpr bool kFirstShared = kRing + kWarps * (kRaw + kFirst) + 8192 <= 232448;
-    static constexpr int kSmem = kRing + kWarps * (kRaw + (kFirstShared ? kFirst : 0));
+    // Scales of k and of v of the tokens of the slices in flight, a place beside each entry of K (and read before the
+    // entry's next copy goes out).
+    static constexpr int kScalePlaces = kEntries / 2;
+    static constexpr int kScales = BLOCK ? kScalePlaces * kSlice * 8 : 0;
+    static_assert(kScalePlaces >= 1 && (kEntries & (kEntries - 1)) == 0, "entries are K and V in turn");
+    static constexpr bool kFirstShared = kRing + kWarps * (kRaw + kScales + kFirst) + 8192 <= 232448;
+    static constexpr int kScalesAt = kRing + kWarps * (kRaw + (kFirstShared ? kFirst : 0));
+    static constexpr int kSmem = kScalesAt + kWarps * kScales;
     static_assert(kSmem + 8192 <= 232448, "shared memory");
 };
 
-template <int DT, int NB, bool FP8, bool TMA>
-__global__ void __launch_bounds__(AttnShape<DT, NB, FP8, TMA>::kThreads, 1)
+template <int DT, int NB, bool FP8, bool TMA, bool BLOCK = false>
+__global__ void __launch_bounds__(AttnShape<DT, NB, FP8, TMA, BLOCK>::kThreads, 1)
 attn_decode_kernel(const __grid_constant__ AttnParams p) {
-    using S = AttnShape<DT, NB, FP8, TMA>;
+    using S = AttnShape<DT, NB, FP8, TMA, BLOCK>;
     using namespace attn;
     constexpr int W = S::kWarps, T = S::kThreads, TS = S::kSlice, MT = TS / 16, E = S::kEntries;
     constexpr int RB = S::kRowBytes;
@@ -292,7 +320,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     pdl_launch_dependents();
     if (lane == 0) {
         // A tensor copy counts its bytes (one arrival arms the barrier), per-thread copies arrive for each lane.
-        for (int i = 0; i < E; ++i) mbar_init(&s_bar[w * E + i], TMA ? 1 : 32);
+        for (int i = 0; i < E; ++i) mbar_init(&s_bar[w * E + i], !TMA ? 32 : BLOCK && i % 2 == 0 ? 33 : 1);
         mbar_init(&s_qbar[w], 32);
         fence_mbar_init_cluster();
         s_req[w] = -1;
@@ -463,7 +491,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         for (int hd = 0; hd < nh; ++hd)
 #pragma unroll 1
             for (int i = lane; i < per; i += 32) copy8(to + hd * S::kRawStride + i * 8, src + (hd * per + i) * 8);
-        if (FP8 && lane < 2 && (lane ? p.v_scale : p.k_scale))
+        if (FP8 && !BLOCK && lane < 2 && (lane ? p.v_scale : p.k_scale))
             copy4(smem_addr(&s_scales[w][lane]), (lane ? p.v_scale : p.k_scale) + hk);
         if (TMA || !kDrop) copies_arrive(smem_addr(&s_qbar[w]));
     };
@@ -593,6 +621,25 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                         if (bad >> ((k >> box_shift) * lines) & 1u) last_valid &= ~(Mask(1) << k);
                 }
                 if (lane == (issued & 31)) valid_of = last_valid;
+                if constexpr (BLOCK) {                               // the scales of tokens lane, lane + 32
+                    const uint32_t to = smem_addr(smem + S::kScalesAt + w * S::kScales +
+                                                  (issued & (S::kScalePlaces - 1)) * TS * 8);
+#pragma unroll
+                    for (int x = 0; x < (TS + 31) / 32; ++x) {
+                        const int tok = x * 32 + lane, b = of + (tok >> box_shift);
+                        const int64_t pg = __shfl_sync(0xffffffffu, now.page, b & 31);
+                        const int slot = __shfl_sync(0xffffffffu, now.in, b & 31) + (tok & (box - 1));
+                        const bool seen = tok < TS && (last_valid >> (tok & (TS - 1)) & 1u);
+                        const int blk = p.block_shift >= 0 ? slot >> p.block_shift : slot / p.block_tokens;
+                        const int64_t at = seen ? pg * p.scale_page_stride + blk * p.scale_block_stride +
+                                                      head * p.scale_head_stride : 0;
+                        if (tok < TS) {
+                            copy4_or_zero(to + tok * 8, p.k_block_scale + at, seen);
+                            copy4_or_zero(to + tok * 8 + 4, p.v_block_scale + at, seen);
+                        }
+                    }
+                    if constexpr (TMA) copies_arrive(bar);
+                }
                 if constexpr (TMA) {
                     box_page = in ? page : p.num_pages;              // outside the view: zeros
                     box_in = in ? place : 0;
@@ -804,6 +851,22 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     }
                 }
             }
+            // Scales of the tokens of this lane's rows: of k, the logarithm of that of v, and one over it. From the
+            // logarithm, so that w / vs does not have its error.
+            float ks[BLOCK ? MT : 1][2], lv[BLOCK ? MT : 1][2], iv[BLOCK ? MT : 1][2];
+            if constexpr (BLOCK) {
+                const float2* const at = reinterpret_cast<const float2*>(smem + S::kScalesAt + w * S::kScales) +
+                                         (taken & (S::kScalePlaces - 1)) * TS;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 of = at[mt * 16 + j * 8 + g];
+                        ks[mt][j] = of.x;
+                        lv[mt][j] = log2_ftz(of.y == 0.f ? 0x1p-100f : of.y);
+                        iv[mt][j] = exp2_ftz(-lv[mt][j]);
+                    }
+            }
             __syncwarp();
             next_entry();
             issue(std::bool_constant<E % 2 == 0>{});                 // into the entry just read: E entries on
@@ -816,12 +879,21 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[mt][j] = sc[mt][nb][j] * col_scale[nb][j & 1];
+                    for (int j = 0; j < 4; ++j) {
+                        x[mt][j] = sc[mt][nb][j] * col_scale[nb][j & 1];
+                        if constexpr (BLOCK) x[mt][j] *= ks[mt][j >> 1];
+                    }
                 if (p.softcap > 0.f) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) x[mt][j] = cap_log2 * tanhf(x[mt][j]);
+                }
+                if constexpr (BLOCK) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[mt][j] += lv[mt][j >> 1];
                 }
                 if (valid != kAll) {
 #pragma unroll
@@ -859,8 +931,13 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) x[mt][j] = exp2_ftz(x[mt][j] - (base[j & 1] - kUp));
-                    l[nb][0] += x[mt][0] + x[mt][2];
-                    l[nb][1] += x[mt][1] + x[mt][3];
+                    if constexpr (BLOCK) {
+                        l[nb][0] += x[mt][0] * iv[mt][0] + x[mt][2] * iv[mt][1];
+                        l[nb][1] += x[mt][1] * iv[mt][0] + x[mt][3] * iv[mt][1];
+                    } else {
+                        l[nb][0] += x[mt][0] + x[mt][2];
+                        l[nb][1] += x[mt][1] + x[mt][3];
+                    }
                     // P as the B operand. FP16 beside an FP8 cache (2^-11 relative, down to 2^-29 of the largest
                     // weight). Beside a BF16 cache P has to be BF16, whose 2^-8 would double the rounding error of
                     // a BF16 output: it goes in two parts, the BF16 number below it and the rest in a second one,
