@@ -3,8 +3,7 @@
 //
 // One pass: codes in, rows out, bound by HBM. A CTA takes kReadRows rows: it
 // finds the request of the first among row_start, its threads the pages of one
-// row each, then every thread brings one group of eight values (16 bytes of a
-// BF16 row) of row after row.
+// row each, then every thread brings the same 16 bytes of row after row.
 #include <cstdint>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,18 +23,38 @@ constexpr int kReadThreads = 256;
 constexpr int kReadRows = 16;
 constexpr unsigned int kStatusBadPage = 2u;
 
-// Eight E4M3 codes as FP32.
-__device__ __forceinline__ void values_of_codes(uint2 v, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint16_t two = static_cast<uint16_t>((i < 2 ? v.x : v.y) >> (i & 1) * 16);
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-        const float2 of = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        f[2 * i] = of.x;
-        f[2 * i + 1] = of.y;
+// N values of a cache as they come: codes, or BF16.
+template <int N, bool FP8>
+struct Held {
+    static constexpr int kBytes = N * (FP8 ? 1 : 2);
+    uint32_t w[kBytes / 4];
+    __device__ __forceinline__ void load(const unsigned char* at) {
+        if constexpr (kBytes == 16) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(at));
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (kBytes == 8) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(at));
+            w[0] = v.x; w[1] = v.y;
+        } else {
+            w[0] = __ldcs(reinterpret_cast<const unsigned int*>(at));
+        }
     }
-}
+    __device__ __forceinline__ void values(float scale, float (&f)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            if constexpr (FP8) {
+                uint32_t h;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w[i / 2] >> (i & 1) * 16)));
+                const float2 of = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                f[2 * i] = of.x * scale;
+                f[2 * i + 1] = of.y * scale;
+            } else {
+                f[2 * i] = bf16_lo(w[i]);
+                f[2 * i + 1] = bf16_hi(w[i]);
+            }
+        }
+    }
+};
 
 template <bool FP8, bool F32>
 __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_constant__ ReadParams p) {
@@ -78,35 +97,40 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
     }
     __syncthreads();
 
-    const int per_head = p.head_dim / 8, per_pool = p.kv_heads * per_head;
+    // A thread's 16 bytes of a row (eight BF16 values, four FP32 ones), kBatch rows at a time in flight.
+    constexpr int N = F32 ? 4 : 8, kBatch = 8;
+    const int per_head = p.head_dim / N, per_pool = p.kv_heads * per_head;
     for (int c = tid; c < 2 * per_pool; c += kReadThreads) {
         const int which = c >= per_pool ? 1 : 0, in = c - which * per_pool, head = in / per_head;
-        unsigned char* const out = p.out[which];
-        if (!out) continue;
-        const unsigned char* const from = p.pool[which] + head * p.head_stride + (in - head * per_head) * (FP8 ? 8 : 16);
+        if (!p.out[which]) continue;
+        unsigned char* const out = p.out[which] + row0 * p.out_stride[which] + in * 16;
+        const unsigned char* const from = p.pool[which] + head * p.head_stride + (in - head * per_head) * Held<N, FP8>::kBytes;
         const float* const scales = FP8 && p.scale[which] ? p.scale[which] + head * p.scale_head_stride : nullptr;
 #pragma unroll
-        for (int i = 0; i < kReadRows; ++i) {
-            const int state = s_state[i];
-            if (state < 0) continue;
-            float f[8] = {};
-            if (state > 0) {
-                if constexpr (FP8) {
-                    values_of_codes(*reinterpret_cast<const uint2*>(from + s_code[i]), f);
-                    const float scale = scales ? scales[s_scale[i]] : 1.f;
+        for (int i0 = 0; i0 < kReadRows; i0 += kBatch) {
+            Held<N, FP8> v[kBatch];
+            float scale[kBatch];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= scale;
-                } else {
-                    unpack8(*reinterpret_cast<const uint4*>(from + s_code[i]), f);
+            for (int i = 0; i < kBatch; ++i) {
+                scale[i] = 1.f;
+                if (s_state[i0 + i] > 0) {
+                    v[i].load(from + s_code[i0 + i]);
+                    if (scales) scale[i] = scales[s_scale[i0 + i]];
                 }
             }
-            unsigned char* const to = out + (row0 + i) * p.out_stride[which];
-            if constexpr (F32) {
-                float4* const o = reinterpret_cast<float4*>(to) + in * 2;
-                o[0] = make_float4(f[0], f[1], f[2], f[3]);
-                o[1] = make_float4(f[4], f[5], f[6], f[7]);
-            } else {
-                store_bf16<8>(to, in * 8, f);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int state = s_state[i0 + i];
+                if (state < 0) continue;
+                float f[N];
+                v[i].values(scale[i], f);
+                if (state == 0) {
+#pragma unroll
+                    for (int j = 0; j < N; ++j) f[j] = 0.f;
+                }
+                unsigned char* const to = out + (i0 + i) * p.out_stride[which];
+                if constexpr (F32) *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+                else store_bf16<8>(to, 0, f);
             }
         }
     }

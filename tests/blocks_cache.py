@@ -125,7 +125,8 @@ def write(cache: BlockCache, codes, scales, rows, slots, peak=None):
             new = need(float(peak[t:t + n, h].max()))
             old = float(s[page, blk, h])
             if held:
-                new = max(old, new)
+                m, e = math.frexp(old)
+                new = max(old if m == 0.5 else math.ldexp(1.0, e), new)   # a power of two in any case
                 if new > old:
                     at = c[page, place - held:place, h]
                     at.copy_(code_of(at.clone().contiguous().view(torch.float8_e4m3fn).float() * (old / new)).view(torch.uint8))
