@@ -42,7 +42,7 @@ int plan_attn(int q_heads, int kv_heads, int head_dim, int kind, int sm_count, A
     const int64_t heads = static_cast<int64_t>(l->grid) * (2 + kAttnWarps) * l->nb * 8;   // pieces of CTAs and warps
     l->workspace_bytes = kAttnTickets * 4 + heads * (2 + l->dt) * 4;
     l->warps = kAttnWarps;
-    l->slice = attn_slice(l->dt, l->nb, l->fp8 != 0, true);
+    l->slice = attn_slice(l->dt, l->nb, l->fp8 != 0, true, l->block != 0);
     return GEMV_OK;
 }
 

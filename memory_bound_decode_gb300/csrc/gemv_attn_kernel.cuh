@@ -238,7 +238,7 @@ struct AttnShape {
     static_assert(FP8 || !BLOCK, "codes have scales");
     static constexpr int kWarps = kAttnWarps;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kSlice = attn_slice(DT, NB, FP8, TMA);
+    static constexpr int kSlice = attn_slice(DT, NB, FP8, TMA, BLOCK);
     static constexpr int kRowBytes = DT * (FP8 ? 1 : 2);
     static constexpr int kEntry = kSlice * kRowBytes;                // K or V of one slice
     static constexpr int kEntries = kAttnRing / kEntry < 8 ? kAttnRing / kEntry : 8;

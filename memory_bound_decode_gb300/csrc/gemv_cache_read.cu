@@ -1,7 +1,10 @@
 // Tokens of a paged cache back as rows of BF16 or FP32: a value is its code
 // times its scale, rounded once.
 //
-// One pass: codes in, rows out, bound by HBM. A CTA takes kReadRows rows: it
+// One pass: codes in, rows out, bound by HBM: 16 requests of up to 4,096 tokens
+// (8 heads of 128 to BF16 rows, 201 MB) 32.3 us, 6.2 TB/s; FP32 rows of 840 MB
+// in all 129 us, 6.5 TB/s; 300 tokens 3.6 us, of which 2 are the launch.
+// A CTA takes kReadRows rows (4, 8, 16, 32: 35.6, 34.0, 34.8, 35.8 us): it
 // finds the request of the first among row_start, its threads the pages of one
 // row each, then every thread brings the same 16 bytes of row after row.
 #include <cstdint>
@@ -20,7 +23,7 @@ static __device__ unsigned int g_read_status;
 namespace {
 
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 16;
+constexpr int kReadRows = 8;
 constexpr unsigned int kStatusBadPage = 2u;
 
 // N values of a cache as they come: codes, or BF16.
@@ -97,8 +100,9 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
     }
     __syncthreads();
 
-    // A thread's 16 bytes of a row (eight BF16 values, four FP32 ones), kBatch rows at a time in flight.
-    constexpr int N = F32 ? 4 : 8, kBatch = 8;
+    // A thread's 16 bytes of a row (eight BF16 values, four FP32 ones), all of the CTA's rows in flight. What is written
+    // leaves the L2 first (16 x 4,096 tokens 33.7 -> 32.3 us).
+    constexpr int N = F32 ? 4 : 8;
     const int per_head = p.head_dim / N, per_pool = p.kv_heads * per_head;
     for (int c = tid; c < 2 * per_pool; c += kReadThreads) {
         const int which = c >= per_pool ? 1 : 0, in = c - which * per_pool, head = in / per_head;
@@ -106,32 +110,32 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
         unsigned char* const out = p.out[which] + row0 * p.out_stride[which] + in * 16;
         const unsigned char* const from = p.pool[which] + head * p.head_stride + (in - head * per_head) * Held<N, FP8>::kBytes;
         const float* const scales = FP8 && p.scale[which] ? p.scale[which] + head * p.scale_head_stride : nullptr;
+        Held<N, FP8> v[kReadRows];
+        float scale[kReadRows];
 #pragma unroll
-        for (int i0 = 0; i0 < kReadRows; i0 += kBatch) {
-            Held<N, FP8> v[kBatch];
-            float scale[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                scale[i] = 1.f;
-                if (s_state[i0 + i] > 0) {
-                    v[i].load(from + s_code[i0 + i]);
-                    if (scales) scale[i] = scales[s_scale[i0 + i]];
-                }
+        for (int i = 0; i < kReadRows; ++i) {
+            scale[i] = 1.f;
+            if (s_state[i] > 0) {
+                v[i].load(from + s_code[i]);
+                if (scales) scale[i] = scales[s_scale[i]];
             }
+        }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int state = s_state[i0 + i];
-                if (state < 0) continue;
-                float f[N];
-                v[i].values(scale[i], f);
-                if (state == 0) {
+        for (int i = 0; i < kReadRows; ++i) {
+            const int state = s_state[i];
+            if (state < 0) continue;
+            float f[N];
+            v[i].values(scale[i], f);
+            if (state == 0) {
 #pragma unroll
-                    for (int j = 0; j < N; ++j) f[j] = 0.f;
-                }
-                unsigned char* const to = out + (i0 + i) * p.out_stride[which];
-                if constexpr (F32) *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-                else store_bf16<8>(to, 0, f);
+                for (int j = 0; j < N; ++j) f[j] = 0.f;
             }
+            unsigned char* const to = out + i * p.out_stride[which];
+            if constexpr (F32)
+                __stcs(reinterpret_cast<float4*>(to), make_float4(f[0], f[1], f[2], f[3]));
+            else
+                __stcs(reinterpret_cast<uint4*>(to),
+                       make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
         }
     }
 }
