@@ -560,9 +560,10 @@ int gemv_probe_sink_words(void);
  *                            h * scale_head_stride]
  *                    (v_block_scale for v; FP32; strides in elements, at least
  *                    1 and at most 2^59, entries that do not overlap). k_scale
- *                    and v_scale are NULL. Scales of visible tokens are
- *                    positive normal numbers (0 counts as 2^-100). The other
- *                    kinds do not read the fields from k_block_scale on.
+ *                    and v_scale are NULL. Scales of visible tokens are positive
+ *                    and finite (those of v below 2^-60, 0 among them, count as
+ *                    2^-60 in gemv_attn_decode). The other kinds do not read
+ *                    the fields from k_block_scale on.
  */
 #define GEMV_CACHE_BF16 0
 #define GEMV_CACHE_FP8 1
@@ -675,11 +676,13 @@ int gemv_block_tables(const gemv_block_tables_args *args, void *stream);
  * undefined). With a the largest magnitude among the finite values of a head's
  * new rows of the block, need = max(2^-30, the smallest power of two that is
  * at least a / 448). Where the first of them takes the block's first slot, the
- * scale becomes need. Else the block holds earlier tokens: the scale becomes
- * max(scale, need), and where it grows the codes of the slots before the first
- * new one become the codes nearest to code * old scale / new scale (between
- * powers of two exactly the same values, but for those that fall among E4M3's
- * subnormals). A repeated call leaves the same bits.
+ * scale becomes need. Else the block holds earlier tokens: the scale becomes the
+ * larger of need and the smallest power of two that is at least the old scale,
+ * and where it grows the codes of the slots before the first new one become the
+ * codes nearest to code * old scale / new scale (between powers of two exactly
+ * the same values, but for those that fall among E4M3's subnormals). So every
+ * scale that a call leaves in a block it writes to is a power of two. A repeated
+ * call leaves the same bits.
  */
 #define GEMV_ROWS_F32 0
 #define GEMV_ROWS_BF16 1

@@ -53,6 +53,7 @@ struct Workspace {
 struct DeviceState {
     bool ready = false;
     bool attn_ready = false;   // the attention kernels too: on the first attention call, which only they serve
+    bool cache_ready = false;  // and those of a cache with scales for blocks, and of reading a cache back, on theirs
     int status = GEMV_OK;
     int sm_count = 0;
     int32_t tc_clusters[4] = {-1, -1, -1, -1};   // resident clusters of 1, 2, 4, 8 tcgen05 CTAs
@@ -92,15 +93,16 @@ int device_state(int* sm_count) {
     return st.status;
 }
 
-// Whether the current device's attention kernels have been set up (and so may have recorded a status).
-bool attn_in_use() {
+// Whether kernels of the current device that are set up on their first call have been (and so may have recorded a
+// status): ready is the device's flag for them.
+bool in_use(bool DeviceState::*ready) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
         cudaGetLastError();
         return false;
     }
     std::lock_guard<std::mutex> lock(g_dev_mutex);
-    return g_dev[dev].attn_ready;
+    return g_dev[dev].*ready;
 }
 
 // The current device's resident-cluster counts for the tcgen05 kernel (set
@@ -644,6 +646,20 @@ int api_attn_state(int* sm_count) {
     std::lock_guard<std::mutex> lock(g_dev_mutex);
     if (!g_dev[dev].attn_ready && (e = prepare_attn()) != cudaSuccess) return cuda_fail(e);
     g_dev[dev].attn_ready = true;
+    return GEMV_OK;
+}
+
+// The same, with every kernel that writes a cache with scales for blocks or reads a cache back loaded, and given its
+// shared memory: a later call of another shape may be captured.
+int api_cache_state(int* sm_count) {
+    int rc = device_state(sm_count), dev = 0;
+    if (rc != GEMV_OK) return rc;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    std::lock_guard<std::mutex> lock(g_dev_mutex);
+    if (g_dev[dev].cache_ready) return GEMV_OK;
+    if ((e = prepare_append_blocks()) != cudaSuccess || (e = prepare_read()) != cudaSuccess) return cuda_fail(e);
+    g_dev[dev].cache_ready = true;
     return GEMV_OK;
 }
 
@@ -1199,8 +1215,8 @@ int gemv_device_status(unsigned int* bits, int reset) {
     if (e == cudaSuccess) e = gemv::read_mma_status_nb2(&b3, reset != 0);
     if (e == cudaSuccess) e = gemv::read_fp8_status(&b4, reset != 0);
     if (e == cudaSuccess) e = gemv::read_tc_status(&b5, reset != 0);
-    if (e == cudaSuccess && attn_in_use()) e = gemv::read_attn_status(&b6, reset != 0);
-    if (e == cudaSuccess) e = gemv::read_read_status(&b7, reset != 0);
+    if (e == cudaSuccess && in_use(&DeviceState::attn_ready)) e = gemv::read_attn_status(&b6, reset != 0);
+    if (e == cudaSuccess && in_use(&DeviceState::cache_ready)) e = gemv::read_read_status(&b7, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e);
     *bits = b1 | b2 | b3 | b4 | b5 | b6 | b7;
     return GEMV_OK;

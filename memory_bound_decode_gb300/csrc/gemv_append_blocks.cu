@@ -37,8 +37,7 @@ constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int append_ctas(bool f32, bool many) { return f32 && many ? 4 : 3; }
 constexpr int kQueryTokens = 2;        // tokens whose query rows a thread has in flight
 constexpr int kMaxWindow = 32;         // tokens of a CTA that writes blocks
-constexpr int kPlainShared = 42 * 1024;   // dynamic shared memory that needs no asking for,
-constexpr int kMostShared = 8 * 8192 + (kMaxWindow - 1 + GEMV_MAX_BLOCK_TOKENS) * GEMV_MAX_HEAD_DIM / 2 * 8;   // and all of it
+constexpr int kMostShared = 8 * 8192 + (kMaxWindow - 1 + GEMV_MAX_BLOCK_TOKENS) * GEMV_MAX_HEAD_DIM / 2 * 8;   // bytes
 static_assert(kMaxWindow + GEMV_MAX_BLOCK_TOKENS <= 96 && kMaxWindow <= 32, "three ballots cover the tokens of a window");
 
 // How a launch is laid out: kv_ctas CTAs write blocks, each `every`-th of the first half or so (they wait for latencies
@@ -632,11 +631,6 @@ cudaError_t launch_one(const RopeParams& p, const BlockScales& b, AppendShape a,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    if (a.shared > kPlainShared) {
-        const cudaError_t e = cudaFuncSetAttribute(append_blocks_kernel<VEC, F32, NI, TT>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
-        if (e != cudaSuccess) return e;
-    }
     return cudaLaunchKernelEx(&cfg, append_blocks_kernel<VEC, F32, NI, TT>, p, b, a);
 }
 
@@ -665,7 +659,24 @@ cudaError_t launch_shape(const RopeParams& p, const BlockScales& b, int sm_count
     return many ? launch_one<VEC, F32, NI, kQueryTokens>(p, b, a, s, pdl) : launch_one<VEC, F32, NI, 1>(p, b, a, s, pdl);
 }
 
+template <int VEC, bool F32, int NI>
+cudaError_t prepare_shape() {
+    const cudaError_t e = cudaFuncSetAttribute(append_blocks_kernel<VEC, F32, NI, 1>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    return e == cudaSuccess ? cudaFuncSetAttribute(append_blocks_kernel<VEC, F32, NI, kQueryTokens>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared)
+                            : e;
+}
+
 }  // namespace
+
+cudaError_t prepare_append_blocks() {
+    cudaError_t e = prepare_shape<8, false, 4>();
+    if (e == cudaSuccess) e = prepare_shape<1, false, 32>();
+    if (e == cudaSuccess) e = prepare_shape<1, true, 32>();
+    if (e == cudaSuccess) e = prepare_shape<4, true, 4>();
+    return e == cudaSuccess ? prepare_shape<4, true, 8>() : e;
+}
 
 cudaError_t launch_append_blocks(const RopeParams& p, const BlockScales& b, int sm_count, cudaStream_t s, bool pdl) {
     // Groups a lane keeps: 8 warps have to hold a block's tokens of a head. Four, which leave room for four CTAs an SM, do

@@ -221,7 +221,8 @@ int gemv_rope_append(const gemv_rope_args* a, const gemv_kv_cache* c, void* stre
     if (!aligned(a->slots, 4)) return GEMV_ERR_ALIGN;
     if (a->tokens == 0) return GEMV_OK;
     int sm_count = 0;
-    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
+    const bool blocks = c->kind == GEMV_CACHE_FP8_BLOCK;
+    if ((rc = blocks ? gemv::api_cache_state(&sm_count) : gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
     gemv::RopeParams p = {};
     fill_rope(a, &p);
     p.v = a->v;
@@ -238,7 +239,7 @@ int gemv_rope_append(const gemv_rope_args* a, const gemv_kv_cache* c, void* stre
     p.head_stride = c->head_stride * es;
     p.slot_stride = c->slot_stride * es;
     p.num_slots = static_cast<int64_t>(c->num_pages) * c->page_size;
-    if (c->kind == GEMV_CACHE_FP8_BLOCK) {
+    if (blocks) {
         const gemv::BlockScales b = {c->k_block_scale, c->v_block_scale, c->scale_page_stride, c->scale_block_stride,
                                      c->scale_head_stride, c->block_tokens, shift_of(c->block_tokens)};
         return finish(gemv::launch_append_blocks(p, b, sm_count, static_cast<cudaStream_t>(stream),
@@ -393,7 +394,7 @@ int gemv_cache_read(const gemv_cache_read_args* a, const gemv_kv_cache* c, void*
         return GEMV_ERR_ALIGN;
     if (a->requests == 0 || a->rows == 0) return GEMV_OK;
     int sm_count = 0;
-    if ((rc = gemv::api_device_state(&sm_count)) != GEMV_OK) return rc;
+    if ((rc = gemv::api_cache_state(&sm_count)) != GEMV_OK) return rc;
     gemv::ReadParams p = {};
     p.pool[0] = static_cast<const unsigned char*>(c->k);
     p.pool[1] = static_cast<const unsigned char*>(c->v);

@@ -13,6 +13,7 @@ namespace gemv {
 // ---- shared with gemv_api.cpp -------------------------------------------------
 int api_device_state(int* sm_count);      // set-up of the current device; GEMV_OK or an error
 int api_attn_state(int* sm_count);        // and of its attention kernels
+int api_cache_state(int* sm_count);       // or of those that write a cache with scales for blocks and read a cache back
 int api_cuda_fail(cudaError_t e);         // record e for gemv_last_cuda_error; GEMV_ERR_CUDA
 bool api_pdl_enabled();
 bool api_on_current_device(const void* p);   // whether p points into the current device's own memory
@@ -137,6 +138,7 @@ struct BlockScales {
     int32_t shift;              // its log2, -1 if it is no power of two
 };
 
+cudaError_t prepare_append_blocks();
 cudaError_t launch_append_blocks(const RopeParams& p, const BlockScales& b, int sm_count, cudaStream_t s, bool pdl);
 
 // ---- rows read back from a cache --------------------------------------------------
@@ -158,6 +160,7 @@ struct ReadParams {
     int32_t fp8, rows_f32;
 };
 
+cudaError_t prepare_read();
 cudaError_t launch_read(const ReadParams& p, cudaStream_t s, bool pdl);
 cudaError_t read_read_status(unsigned int* bits, bool reset);
 

@@ -868,7 +868,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     for (int j = 0; j < 2; ++j) {
                         const float2 of = at[mt * 16 + j * 8 + g];
                         ks[mt][j] = of.x;
-                        lv[mt][j] = log2_ftz(of.y == 0.f ? 0x1p-100f : of.y);
+                        lv[mt][j] = log2_ftz(of.y < 0x1p-60f ? 0x1p-60f : of.y);
                         iv[mt][j] = exp2_ftz(-lv[mt][j]);
                     }
             }

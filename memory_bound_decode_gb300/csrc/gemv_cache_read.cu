@@ -156,6 +156,14 @@ cudaError_t launch_one(const ReadParams& p, cudaStream_t s, bool pdl) {
 
 }  // namespace
 
+cudaError_t prepare_read() {
+    cudaFuncAttributes a;                                            // (asking for them loads the kernel)
+    cudaError_t e = cudaFuncGetAttributes(&a, cache_read_kernel<true, true>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, cache_read_kernel<true, false>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, cache_read_kernel<false, true>);
+    return e == cudaSuccess ? cudaFuncGetAttributes(&a, cache_read_kernel<false, false>) : e;
+}
+
 cudaError_t launch_read(const ReadParams& p, cudaStream_t s, bool pdl) {
     if (p.fp8) return p.rows_f32 ? launch_one<true, true>(p, s, pdl) : launch_one<true, false>(p, s, pdl);
     return p.rows_f32 ? launch_one<false, true>(p, s, pdl) : launch_one<false, false>(p, s, pdl);

@@ -201,7 +201,8 @@ class AttentionStep:
     With ``advance`` every step appends a token (lengths and the place in the
     free list move on in place, so a replayed graph is one step after the
     other), for up to ``room`` steps; without, every step writes the same token
-    again. ``cache``: "bf16" or "fp8" (E4M3, a scale per key-value head).
+    again. ``cache``: "bf16", "fp8" (E4M3, a scale per key-value head) or "fp8_block" (E4M3, a scale for each block of
+    tokens, a page or a part of one, and key-value head, found as they are written).
     """
 
     def __init__(self, spec: dict, context, batch: int = 1, seed: int = 0, device="cuda", cache: str = "bf16",
@@ -209,8 +210,8 @@ class AttentionStep:
                  rope_base: float = 500000.0):
         if not 1 <= batch <= binding.GEMV_MAX_BATCH:
             raise ValueError("batch must be 1..16")
-        if cache not in ("bf16", "fp8"):
-            raise ValueError("cache must be bf16 or fp8")
+        if cache not in ("bf16", "fp8", "fp8_block"):
+            raise ValueError("cache must be bf16, fp8 or fp8_block")
         lens = [context] * batch if isinstance(context, int) else list(context)
         if len(lens) != batch or min(lens) < 0:
             raise ValueError("context must be a length, or one per request")
@@ -254,7 +255,10 @@ class AttentionStep:
 
         self.inv_freq = [rope_base ** (-2.0 * i / head_dim) for i in range(head_dim // 2)]
         self.freqs = binding.rope_freqs(self.inv_freq, device=device)
-        self.workspace = binding.attn_workspace(self.q_heads, self.kv_heads, head_dim, device=device)
+        self.block_tokens = max(n for n in range(1, binding.GEMV_MAX_BLOCK_TOKENS + 1) if page_size % n == 0)
+        self.kind = {"bf16": binding.GEMV_CACHE_BF16, "fp8": binding.GEMV_CACHE_FP8,
+                     "fp8_block": binding.GEMV_CACHE_FP8_BLOCK}[cache]
+        self.workspace = binding.attn_workspace(self.q_heads, self.kv_heads, head_dim, self.kind, device=device)
         self.layers = []
         for l in range(spec["layers"]):
             self.layers.append(self._layer(l, seed, g))
@@ -273,18 +277,24 @@ class AttentionStep:
                  out=torch.empty((B, Q), dtype=torch.bfloat16, device=dev),
                  o=torch.empty((B, H), dtype=torch.float32, device=dev))
         shape = (self.num_pages, self.page_size, self.kv_heads, D)
-        scales = [None, None]
+        scales, per_page = [None, None], self.page_size // self.block_tokens
         for i, n in enumerate(("k", "v")):
             d[n] = torch.randn(shape, generator=g, device=dev, dtype=torch.bfloat16)
-            if self.cache == "fp8":
+            if self.cache != "bf16":
                 d[n] = (d[n] * 32).to(torch.float8_e4m3fn)
-                scales[i] = torch.full((self.kv_heads,), 1.0 / 32, device=dev)
+                scales[i] = torch.full((self.kv_heads,) if self.cache == "fp8" else
+                                       (self.num_pages, per_page, self.kv_heads), 1.0 / 32, device=dev)
         d["scales"] = scales
+        if self.cache == "fp8_block":
+            scaled = dict(k_block_scale=scales[0], v_block_scale=scales[1], block_tokens=self.block_tokens,
+                          scale_page_stride=per_page * self.kv_heads, scale_block_stride=self.kv_heads,
+                          scale_head_stride=1)
+        else:
+            scaled = dict(k_scale=scales[0], v_scale=scales[1])
         d["cache"] = binding.kv_cache(
             d["k"], d["v"], num_pages=self.num_pages, page_size=self.page_size, kv_heads=self.kv_heads, head_dim=D,
             page_stride=self.page_size * KV, head_stride=D, slot_stride=KV,
-            kind=binding.GEMV_CACHE_FP8 if self.cache == "fp8" else binding.GEMV_CACHE_BF16,
-            k_scale=scales[0], v_scale=scales[1])
+            kind=self.kind, **scaled)
         d["rope"] = binding.rope_args(
             q=d["y"][0], k=d["y"][1], v=d["y"][2], q_out=d["q"], positions=self.positions, freqs=self.freqs,
             tokens=B, q_heads=self.q_heads, kv_heads=self.kv_heads, head_dim=D, rot_dim=D, q_stride=Q, k_stride=KV,
@@ -327,8 +337,11 @@ class AttentionStep:
         DecodeStep; q, k and v rows read, q and the new slots written; the
         visible tokens' K and V and q read, the attention's output written."""
         H, Q, KV, B = self.spec["hidden"], self.spec["q_rows"], self.spec["kv_rows"], self.batch
-        es = 1 if self.cache == "fp8" else 2
+        es = 2 if self.cache == "bf16" else 1
+        scales = 0
+        if self.cache == "fp8_block":    # those of the visible tokens read, of the new tokens' blocks read and written
+            scales = 8 * self.kv_heads * (sum(-(-(n + 1) // self.block_tokens) for n in self.context) + 2 * B)
         layer = (roofline.algorithmic_bytes(Q + 2 * KV, H, B) + roofline.algorithmic_bytes(H, Q, B)
                  + B * (4 * (Q + 2 * KV) + 2 * Q + 2 * KV * es)
-                 + 2 * sum(n + 1 for n in self.context) * KV * es + B * 4 * Q)
+                 + 2 * sum(n + 1 for n in self.context) * KV * es + B * 4 * Q + scales)
         return len(self.layers) * layer

@@ -262,3 +262,28 @@ def test_repeated_captured_and_elsewhere():
     side = torch.cuda.Stream()
     binding.gemv_rope_append(args, rec, side)
     again()
+
+
+def test_other_shapes_are_captured_after_a_first_call():
+    """Kernels that no call has used yet may be used in a capture: the first call on the device has loaded them all."""
+    cache = bc.BlockCache([2000, 70], 64, 64, 2, 256, "token", seed=13)
+    recs = []
+    for T, f32, offset in ((1900, True, 0), (1900, False, 0), (3, True, 1), (3, False, 1)):
+        c = Case(T, 2, 2, 256, 256, f32=f32, seed=T, offset=offset)
+        slots = cache.slots_of(0, 5, 1900) if T > 3 else cache.slots_of(1, 64, 3)
+        slots_t = torch.tensor(slots, dtype=torch.int32).cuda()
+        recs.append((c, slots, slots_t, c.args(v=c.v, v_stride=c.sk, slots=slots_t)))
+    rec = cache.record()
+    first = Case(1, 2, 2, 64, 64, seed=1)
+    small = bc.BlockCache([1], 8, 8, 2, 64)
+    binding.gemv_rope_append(first.args(v=first.v, v_stride=first.sk, slots=torch.tensor(small.slots_of(0, 0, 1),
+                                        dtype=torch.int32).cuda()), small.record())
+    for c, slots, _, args in recs:
+        torch.cuda.synchronize()
+        before = cache.host()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+            binding.gemv_rope_append(args, rec)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(c, cache, slots, before, cache.host())

@@ -121,6 +121,20 @@ def test_blocks_of_zeros_with_a_scale_of_zero():
     a.check()
 
 
+def test_nothing_but_zeros_under_scales_of_zero():
+    """Every scale of v 0, many tokens: the sum of weights stays in range, the log-sum-exp is k's."""
+    lens = [9000]
+    cache = bc.BlockCache(lens, 64, 64, 2, 64, "head", seed=8)
+    cache.pools[1].zero_()
+    cache.scales[1].zero_()
+    cache.values[1][0].zero_()
+    a = Attn(lens, cache, 8, seed=3)
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
+    assert (a.out == 0).all()
+
+
 def test_scales_that_are_no_numbers_reach_their_own_head_only():
     lens = [40, 40]
     cache = bc.BlockCache(lens, 16, 16, 2, 64, "token", seed=9)
