@@ -43,14 +43,15 @@ static_assert(kMaxWindow + GEMV_MAX_BLOCK_TOKENS <= 96 && kMaxWindow <= 32, "thr
 // How a launch is laid out: kv_ctas CTAs write blocks, each `every`-th of the first half or so (they wait for latencies
 // while the others stream: a FP32 prompt 29.4 us with all of them first, 28.2 so), the others turn queries.
 struct AppendShape {
-    unsigned kv_ctas, every;
+    unsigned kv_ctas;
+    int every_shift;                   // log2 of `every`
     int window;                        // tokens of a CTA that writes blocks
-    int kv_parts;                      // CTAs that share a window's heads: the first half k's, the others v's
+    int kv_parts, kv_shift;            // CTAs that share a window's heads: the first half k's, the others v's
     int groups, across;                // of a head; tokens that a warp takes side by side
     int tokens_held;                   // of a head, by a warp
-    uint32_t per_group;                // u * per_group >> 32 is u / groups (groups > 1)
+    uint32_t per_group, per_head;      // u * per_group >> 32 is u / groups (groups > 1), with per_head u / kv_heads
     int turns, shared;                 // cosines in shared memory; its bytes
-    int parts, visit;                  // CTAs of a token's queries, query heads of each
+    int parts, parts_shift, visit;     // CTAs of a token's queries, query heads of each
 };
 
 // Cosine and sine of a position times a frequency. The angle is a fraction of a turn in 64 bits, so position * freq modulo
@@ -226,6 +227,11 @@ __device__ __forceinline__ void kept_group(const unsigned char* line, int lane, 
     b.values(y);
 }
 
+__device__ __forceinline__ void keep_turned(unsigned char* line, int lane, const float (&x)[4], const float (&y)[4]) {
+    *reinterpret_cast<float4*>(line + lane * 16) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(line + 512 + lane * 16) = make_float4(y[0], y[1], y[2], y[3]);
+}
+
 // Threads of a team's warps wait for each other.
 __device__ __forceinline__ void team_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
@@ -249,7 +255,8 @@ __device__ __forceinline__ void write_singles(const RopeParams& p, const BlockSc
     const int items = __popc(runs) * p.kv_heads, before = __popc(runs & ((1u << lane) - 1u));
 #pragma unroll 1
     for (int base = (share * kAppendWarps + warp) * a.across; base < items; base += shares * kAppendWarps * a.across) {
-        const int item = base + sub, ri = item / p.kv_heads, head = item - ri * p.kv_heads;
+        const int item = base + sub, ri = p.kv_heads == 1 ? item : static_cast<int>(__umulhi(static_cast<uint32_t>(item), a.per_head));
+        const int head = item - ri * p.kv_heads;
         const bool live = sub < a.across && item < items;
         // The lane of the item's run: the one with `ri` of them before it.
         int run = 0;
@@ -315,13 +322,14 @@ __device__ __forceinline__ void write_singles(const RopeParams& p, const BlockSc
 template <int VEC, bool F32, int NI>
 __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockScales& b, const AppendShape& a, int cta) {
     constexpr int es = F32 ? 4 : 2;
+    constexpr bool kTurnOnce = F32 && VEC > 1;                       // turned rows have room where they were
     extern __shared__ __align__(16) unsigned char s_rows[];          // every warp's lines; then
     float* const s_cos = reinterpret_cast<float*>(s_rows + kAppendWarps * NI * kLineBytes<VEC>);   // [token][pair], and sines
     float* const s_sin = s_cos + a.turns;
     __shared__ uint32_t s_top[2][kAppendWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned char* const lines = s_rows + warp * NI * kLineBytes<VEC>;
-    const int win = cta / a.kv_parts, part = cta - win * a.kv_parts, shares = a.kv_parts >> 1;
+    const int win = a.kv_shift >= 0 ? cta >> a.kv_shift : cta / a.kv_parts, part = cta - win * a.kv_parts, shares = a.kv_parts >> 1;
     const bool is_k = part < shares;                                 // the others take v
     const int share = is_k ? part : part - shares;
     const int64_t first = static_cast<int64_t>(win) * a.window;
@@ -338,6 +346,8 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
         const int reach = a.window - 1 + b.tokens;                   // no run of the window goes further
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
+            goes_on[x] = 0u;
+            if (x * 32 >= reach) continue;
             const int j = x * 32 + lane;
             bool on = false;
             if (j < reach && first + j < p.tokens) {
@@ -402,7 +412,7 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
     // The head and the run (its first token, from the window's on) of the team's item.
     int item = share * at_once + team, head = 0, run = 0, n_run = 0;
     auto locate = [&]() {
-        const int ri = item / p.kv_heads;
+        const int ri = p.kv_heads == 1 ? item : static_cast<int>(__umulhi(static_cast<uint32_t>(item), a.per_head));
         head = item - ri * p.kv_heads;
         run = __ffs(__ballot_sync(0xffffffffu, (runs >> lane & 1u) && __popc(runs & ((1u << lane) - 1u)) == ri)) - 1;
         n_run = __shfl_sync(0xffffffffu, n, run);
@@ -433,10 +443,29 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
     const int table0 = __ffs(runs) - 1;                              // the first token of the table of sines
     if (is_k) {
         const int end = __reduce_max_sync(0xffffffffu, n > 0 ? lane + n : 0);
-        const int dt = kAppendThreads / half, dp = kAppendThreads - dt * half;   // the same pair again where their number divides
+        const int dt = kAppendThreads / half, dp = kAppendThreads - dt * half;
         int t = tid / half, pair = tid - t * half, to = tid;
         t += table0;
         constexpr int U = 4;                                         // at a time, so that their loads are
+        if (dp == 0) {                                               // the same pair again and again
+            const int axis = p.pair_axis ? min(max(p.pair_axis[pair], 0), p.axes - 1) : 0;
+            const uint64_t freq = static_cast<uint64_t>(p.freqs[pair]);
+            const int32_t* const at = p.positions + axis * p.axis_stride + first;
+            for (; t < end; t += U * dt) {
+                int32_t pos[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i) pos[i] = at[min(t + i * dt, end - 1)];
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const float2 cs = turn_of(pos[i], freq);
+                    if (t + i * dt < end) {
+                        s_cos[to + i * kAppendThreads] = cs.x;
+                        s_sin[to + i * kAppendThreads] = cs.y;
+                    }
+                }
+                to += U * kAppendThreads;
+            }
+        }
         while (t < end) {
             int32_t pos[U];
             uint64_t freq[U];
@@ -492,6 +521,8 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
             if (!in_row || tk >= n_run) continue;
             float x[VEC], y[VEC];
             turned(i, tk, gi, x, y);
+            if constexpr (kTurnOnce)
+                if (is_k) keep_turned(lines + i * kLineBytes<VEC>, lane, x, y);
             most = fmaxf(most, largest_finite<VEC>(x, y));
         }
         uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
@@ -522,7 +553,8 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
                 }
                 if (in_row && tk < n_run) {
                     float x[VEC], y[VEC];
-                    turned(i, tk, gi, x, y);
+                    if constexpr (kTurnOnce) kept_group<VEC, F32>(lines + i * kLineBytes<VEC>, lane, x, y);
+                    else turned(i, tk, gi, x, y);
                     store_codes<VEC>(to + c0, x, inv);
                     store_codes<VEC>(to + c1, y, inv);
                 }
@@ -542,26 +574,26 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
 
 // The queries of TT tokens, `visit` heads a CTA: as gemv_rope turns them.
 template <int VEC, bool F32, int TT>
-__device__ __forceinline__ void turn_queries(const RopeParams& p, int64_t tok0, int part, int visit) {
+__device__ __forceinline__ void turn_queries(const RopeParams& p, const AppendShape& a, int64_t tok0, int part) {
     constexpr int GAP = VEC > 1 ? 2 : 0;                             // a warp's groups lie in different banks
     __shared__ __align__(16) float2 s_turn[TT][GEMV_MAX_HEAD_DIM / 2 / VEC * (VEC + GAP)];
     constexpr int es = F32 ? 4 : 2;
-    const int groups = p.head_dim / (2 * VEC), half = p.rot_dim / 2;
-    const int hy = static_cast<int>(threadIdx.x) / groups, gi = threadIdx.x - hy * groups;
-    const int h = part * visit + hy;
-    const bool is_head = hy < visit && h < p.q_heads;
+    const int groups = a.groups, half = p.rot_dim / 2;
+    const int hy = groups == 1 ? threadIdx.x : __umulhi(threadIdx.x, a.per_group), gi = threadIdx.x - hy * groups;
+    const int h = part * a.visit + hy;
+    const bool is_head = hy < a.visit && h < p.q_heads;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(TT), p.tokens - tok0));
     const bool turned = gi * VEC < half;
     const int c0 = turned && !p.interleaved ? gi * VEC : gi * 2 * VEC;
     const int c1 = turned && !p.interleaved ? half + gi * VEC : gi * 2 * VEC + VEC;
-    Cols<VEC, F32> a[TT], c[TT];
+    Cols<VEC, F32> u[TT], v[TT];
     int slot[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
         if (is_head && i < tokens) {
             const char* const row = static_cast<const char*>(p.q) + ((tok0 + i) * p.q_stride + h * p.head_dim) * es;
-            a[i].load(row, c0);
-            c[i].load(row, c1);
+            u[i].load(row, c0);
+            v[i].load(row, c1);
         }
         slot[i] = i < tokens ? p.slots[tok0 + i] : -1;
     }
@@ -581,8 +613,8 @@ __device__ __forceinline__ void turn_queries(const RopeParams& p, int64_t tok0, 
     for (int i = 0; i < TT; ++i) {
         if (!is_head || slot[i] < 0 || slot[i] >= p.num_slots) continue;   // a padding row: nothing of it is written
         float x[VEC], y[VEC];
-        a[i].values(x);
-        c[i].values(y);
+        u[i].values(x);
+        v[i].values(y);
         if (turned) {
             float cs[VEC], sn[VEC];
 #pragma unroll
@@ -605,12 +637,13 @@ __global__ void __launch_bounds__(kAppendThreads, append_ctas(F32, TT > 1)) appe
                                                                     const __grid_constant__ AppendShape a) {
     pdl_launch_dependents();
     pdl_wait_prerequisites();
-    const unsigned turn = blockIdx.x / a.every;
-    if (turn * a.every == blockIdx.x && turn < a.kv_ctas) {
+    const unsigned turn = blockIdx.x >> a.every_shift;
+    if (turn << a.every_shift == blockIdx.x && turn < a.kv_ctas) {
         write_blocks<VEC, F32, NI>(p, b, a, static_cast<int>(turn));
     } else {
-        const unsigned q = blockIdx.x - min((blockIdx.x + a.every - 1) / a.every, a.kv_ctas), at = q / a.parts;
-        turn_queries<VEC, F32, TT>(p, static_cast<int64_t>(at) * TT, static_cast<int>(q - at * a.parts), a.visit);
+        const unsigned q = blockIdx.x - min(blockIdx.x + (1u << a.every_shift) - 1 >> a.every_shift, a.kv_ctas);
+        const unsigned at = a.parts_shift >= 0 ? q >> a.parts_shift : q / a.parts;
+        turn_queries<VEC, F32, TT>(p, a, static_cast<int64_t>(at) * TT, static_cast<int>(q - at * a.parts));
     }
 }
 
@@ -620,7 +653,8 @@ cudaError_t launch_one(const RopeParams& p, const BlockScales& b, AppendShape a,
     const int64_t q = (static_cast<int64_t>(p.tokens) + TT - 1) / TT * a.parts;
     if (kv + q > 0x7fffffff) return cudaErrorInvalidConfiguration;
     a.kv_ctas = static_cast<unsigned>(kv);
-    a.every = static_cast<unsigned>(1 + q / (2 * kv));
+    a.every_shift = 0;
+    while (q >= (int64_t(2) << a.every_shift) * 2 * kv) ++a.every_shift;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(kv + q), 1, 1);
     cfg.blockDim = dim3(kAppendThreads, 1, 1);
@@ -634,13 +668,22 @@ cudaError_t launch_one(const RopeParams& p, const BlockScales& b, AppendShape a,
     return cudaLaunchKernelEx(&cfg, append_blocks_kernel<VEC, F32, NI, TT>, p, b, a);
 }
 
+// log2 of a power of two, -1 of other numbers (254 single tokens 4.6 us with divisions, 4.4 with shifts).
+int shift_of(int n) {
+    int s = 0;
+    while (1 << s < n) ++s;
+    return 1 << s == n ? s : -1;
+}
+
 template <int VEC, bool F32, int NI>
 cudaError_t launch_shape(const RopeParams& p, const BlockScales& b, int sm_count, cudaStream_t s, bool pdl) {
     AppendShape a = {};
     a.groups = p.head_dim / (2 * VEC);
     const int most = kAppendThreads / a.groups;                            // query heads of a CTA
     a.parts = (p.q_heads + most - 1) / most;
+    a.parts_shift = shift_of(a.parts);
     a.visit = (p.q_heads + a.parts - 1) / a.parts;
+    a.per_head = p.kv_heads > 1 ? static_cast<uint32_t>((uint64_t(1) << 32) / p.kv_heads + 1) : 0;
     a.per_group = a.groups > 1 ? static_cast<uint32_t>((uint64_t(1) << 32) / a.groups + 1) : 0;
     a.across = VEC > 1 ? 32 / a.groups : 1;
     a.tokens_held = VEC > 1 ? NI * a.across : std::max(1, NI * 32 / a.groups);
@@ -648,6 +691,7 @@ cudaError_t launch_shape(const RopeParams& p, const BlockScales& b, int sm_count
     const int slices = (b.tokens + a.tokens_held - 1) / a.tokens_held;
     const int at_once = slices <= 1 ? kAppendWarps : slices <= 2 ? kAppendWarps / 2 : slices <= 4 ? kAppendWarps / 4 : kAppendWarps / 8;
     a.kv_parts = 2 * ((p.kv_heads + at_once - 1) / at_once);
+    a.kv_shift = shift_of(a.kv_parts);
     // Windows as wide as it takes for one wave of CTAs, up to a block's tokens: a CTA without a run costs a microsecond
     // of its place, runs one after the other cost two each.
     const bool many = static_cast<int64_t>(p.tokens) * a.parts >= 4 * sm_count;
