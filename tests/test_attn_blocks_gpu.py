@@ -81,6 +81,23 @@ def test_work_split(requests, length):
     assert torch.equal(first.view(torch.int16), a.guard.view(torch.int16)), "the same bits"
 
 
+@pytest.mark.parametrize("requests,heads", [(2, 8), (16, 8), (32, 1), (33, 2), (100, 6), (256, 4), (257, 2)])
+@pytest.mark.parametrize("longest", [1, 64, 130, 1024, 1025])
+def test_rows_taken_whole(requests, heads, longest):
+    """Ragged rows on both sides of the lengths, and numbers of requests, up to which a CTA takes whole ones."""
+    if requests * longest * heads > 700000:
+        pytest.skip("the reference takes long")
+    g = torch.Generator().manual_seed(requests + longest)
+    lens = torch.randint(0, longest + 1, (requests,), generator=g).tolist()
+    lens[requests // 2] = longest
+    lens[0] = 0
+    cache = bc.BlockCache(lens, 64, 16, heads, 64, "head", seed=longest)
+    a = Attn(lens, cache, 2 * heads, seed=3)
+    a.run()
+    torch.cuda.synchronize()
+    a.check()
+
+
 @pytest.mark.parametrize("spread", [(-40, 40), (-25, -20), (20, 25), (-3, 3)])
 def test_scales_far_apart(spread):
     """v's blocks differ by up to 2^80: weights are relative to the largest product, so the bound holds throughout."""
