@@ -287,3 +287,20 @@ def test_other_shapes_are_captured_after_a_first_call():
         graph.replay()
         torch.cuda.synchronize()
         check(c, cache, slots, before, cache.host())
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("T,interleaved", [(3, False), (700, True)])
+def test_queries_are_those_of_the_other_caches(f32, T, interleaved):
+    """q is turned the same way whatever the cache: the same bits."""
+    c = Case(T, 32, 2, 128, 128, f32=f32, interleaved=interleaved, seed=T, far=100000)
+    other = au.Cache([T], 16, 2, 128, "fp8", "token", seed=7)
+    cache = bc.BlockCache([T], 16, 16, 2, 128, "token", seed=7)
+    slots = torch.tensor(cache.slots_of(0, 0, T), dtype=torch.int32).cuda()
+    binding.gemv_rope_append(c.args(v=c.v, v_stride=c.sk, slots=slots), other.record())
+    torch.cuda.synchronize()
+    want = c.q_out.clone()
+    c.q_out.fill_(-777.0)
+    binding.gemv_rope_append(c.args(v=c.v, v_stride=c.sk, slots=slots), cache.record())
+    torch.cuda.synchronize()
+    assert torch.equal(want.view(torch.int16), c.q_out.view(torch.int16))
