@@ -559,8 +559,9 @@ int gemv_probe_sink_words(void);
  *                            s / block_tokens * scale_block_stride +
  *                            h * scale_head_stride]
  *                    (v_block_scale for v; FP32; strides in elements, at least
- *                    1 and at most 2^59, entries that do not overlap). k_scale
- *                    and v_scale are NULL. Scales of visible tokens are positive
+ *                    1 where there is more than one entry to step over and at
+ *                    most 2^59; entries that do not overlap). k_scale and
+ *                    v_scale are NULL. Scales of visible tokens are positive
  *                    and finite (those of v below 2^-60, 0 among them, count as
  *                    2^-60 in gemv_attn_decode). The other kinds do not read
  *                    the fields from k_block_scale on.
@@ -680,9 +681,10 @@ int gemv_block_tables(const gemv_block_tables_args *args, void *stream);
  * larger of need and the smallest power of two that is at least the old scale,
  * and where it grows the codes of the slots before the first new one become the
  * codes nearest to code * old scale / new scale (between powers of two exactly
- * the same values, but for those that fall among E4M3's subnormals). So every
- * scale that a call leaves in a block it writes to is a power of two. A repeated
- * call leaves the same bits.
+ * the same values, but for those that fall among E4M3's subnormals). Slots
+ * behind the last new one keep their codes, whatever becomes of the scale. So
+ * every scale that a call leaves in a block it writes to is a power of two. A
+ * repeated call leaves the same bits.
  */
 #define GEMV_ROWS_F32 0
 #define GEMV_ROWS_BF16 1
@@ -728,8 +730,8 @@ int gemv_rope_freqs(const double *inv_freq, int n, int64_t *freqs);
  * Tokens of a cache back as rows, for the next piece of a prompt, say: row i of
  * k_out and v_out, row_start[r] <= i < row_start[r + 1], becomes k and v of
  * token begin[r] + i - row_start[r] of request r, whose pages are
- * table[r * table_stride + b]: a value of the cache (for FP8 code times scale),
- * rounded once to the rows' type (row_type: GEMV_ROWS_*).
+ * table[r * table_stride + b]: a value of the cache (for FP8 the FP32 product of
+ * code and scale) rounded to the rows' type (row_type: GEMV_ROWS_*).
  *   k_out, v_out: rows of kv_heads x head_dim values, strides in elements
  *           (multiples of 16 bytes), 16-byte aligned; one of them may be NULL.
  *   begin:  requests entries, or NULL: every request from its token 0.

@@ -251,7 +251,8 @@ __device__ __forceinline__ void write_singles(const RopeParams& p, const BlockSc
     const int items = __popc(runs) * p.kv_heads, before = __popc(runs & ((1u << lane) - 1u));
 #pragma unroll 1
     for (int base = (share * kAppendWarps + warp) * a.across; base < items; base += shares * kAppendWarps * a.across) {
-        const int item = base + sub, ri = p.kv_heads == 1 ? item : static_cast<int>(__umulhi(static_cast<uint32_t>(item), a.per_head));
+        const int item = base + sub;
+        const int ri = p.kv_heads == 1 ? item : static_cast<int>(__umulhi(static_cast<uint32_t>(item), a.per_head));
         const int head = item - ri * p.kv_heads;
         const bool live = sub < a.across && item < items;
         // The lane of the item's run: the one with `ri` of them before it.
@@ -280,7 +281,8 @@ __device__ __forceinline__ void write_singles(const RopeParams& p, const BlockSc
                 for (int j = 0; j < VEC; ++j) {
                     const int pair = gi * VEC + j;
                     const int axis = p.pair_axis ? min(max(p.pair_axis[pair], 0), p.axes - 1) : 0;
-                    const float2 of = turn_of(p.positions[axis * p.axis_stride + first + run], static_cast<uint64_t>(p.freqs[pair]));
+                    const int32_t pos = p.positions[axis * p.axis_stride + first + run];
+                    const float2 of = turn_of(pos, static_cast<uint64_t>(p.freqs[pair]));
                     cs[j] = of.x;
                     sn[j] = of.y;
                 }
@@ -300,7 +302,8 @@ __device__ __forceinline__ void write_singles(const RopeParams& p, const BlockSc
         const float scale = held_run > 0 ? fmaxf(power_above(old), need) : need;
         const float inv = one_over(scale);
         // Earlier tokens move to the new scale: the whole warp for each team whose scale grew.
-        for (uint32_t rest = __ballot_sync(0xffffffffu, live && gi == 0 && held_run > 0 && scale > old); rest; rest &= rest - 1) {
+        const uint32_t grown = __ballot_sync(0xffffffffu, live && gi == 0 && held_run > 0 && scale > old);
+        for (uint32_t rest = grown; rest; rest &= rest - 1) {
             const int at = __ffs(rest) - 1;
             unsigned char* const block =
                 reinterpret_cast<unsigned char*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(block_at), at));
@@ -325,7 +328,8 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
     __shared__ uint32_t s_top[2][kAppendWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned char* const lines = s_rows + warp * NI * kLineBytes<VEC>;
-    const int win = a.kv_shift >= 0 ? cta >> a.kv_shift : cta / a.kv_parts, part = cta - win * a.kv_parts, shares = a.kv_parts >> 1;
+    const int win = a.kv_shift >= 0 ? cta >> a.kv_shift : cta / a.kv_parts;
+    const int part = cta - win * a.kv_parts, shares = a.kv_parts >> 1;
     const bool is_k = part < shares;                                 // the others take v
     const int share = is_k ? part : part - shares;
     const int64_t first = static_cast<int64_t>(win) * a.window;
@@ -628,9 +632,9 @@ __device__ __forceinline__ void turn_queries(const RopeParams& p, const AppendSh
 }
 
 template <int VEC, bool F32, int NI, int TT>
-__global__ void __launch_bounds__(kAppendThreads, append_ctas(F32, TT > 1)) append_blocks_kernel(const __grid_constant__ RopeParams p,
-                                                                    const __grid_constant__ BlockScales b,
-                                                                    const __grid_constant__ AppendShape a) {
+__global__ void __launch_bounds__(kAppendThreads, append_ctas(F32, TT > 1))
+append_blocks_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ BlockScales b,
+                     const __grid_constant__ AppendShape a) {
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     const unsigned turn = blockIdx.x >> a.every_shift;
@@ -685,7 +689,7 @@ cudaError_t launch_shape(const RopeParams& p, const BlockScales& b, int sm_count
     a.tokens_held = VEC > 1 ? NI * a.across : std::max(1, NI * 32 / a.groups);
     // As many CTAs as take all heads of a whole block at once.
     const int slices = (b.tokens + a.tokens_held - 1) / a.tokens_held;
-    const int at_once = slices <= 1 ? kAppendWarps : slices <= 2 ? kAppendWarps / 2 : slices <= 4 ? kAppendWarps / 4 : kAppendWarps / 8;
+    const int at_once = kAppendWarps / (slices <= 1 ? 1 : slices <= 2 ? 2 : slices <= 4 ? 4 : 8);
     a.kv_parts = 2 * ((p.kv_heads + at_once - 1) / at_once);
     a.kv_shift = shift_of(a.kv_parts);
     // Windows as wide as it takes for one wave of CTAs, up to a block's tokens: a CTA without a run costs a microsecond
@@ -722,10 +726,11 @@ cudaError_t launch_append_blocks(const RopeParams& p, const BlockScales& b, int 
     // Groups a lane keeps: 8 warps have to hold a block's tokens of a head. Four, which leave room for four CTAs an SM, do
     // but for FP32 heads of over 128 columns in blocks of over 32.
     if (!p.rows_f32)
-        return p.vec >= 8 ? launch_shape<8, false, 4>(p, b, sm_count, s, pdl) : launch_shape<1, false, 32>(p, b, sm_count, s, pdl);
+        return p.vec >= 8 ? launch_shape<8, false, 4>(p, b, sm_count, s, pdl)
+                          : launch_shape<1, false, 32>(p, b, sm_count, s, pdl);
     if (p.vec < 4) return launch_shape<1, true, 32>(p, b, sm_count, s, pdl);
     return kAppendWarps * 4 * (32 / (p.head_dim / 8)) >= b.tokens ? launch_shape<4, true, 4>(p, b, sm_count, s, pdl)
-                                                            : launch_shape<4, true, 8>(p, b, sm_count, s, pdl);
+                                                                  : launch_shape<4, true, 8>(p, b, sm_count, s, pdl);
 }
 
 }  // namespace gemv
