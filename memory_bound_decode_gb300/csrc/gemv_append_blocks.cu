@@ -20,8 +20,8 @@
 // take the lanes that hold a row, and registers.
 //
 // Measured: 4,054 tokens of 32 + 8 + 8 FP32 heads of 128 in blocks of 16 (141 MB)
-// 28.9 us, 4.9 TB/s, bound by instructions (issue 55% busy) and four CTAs an SM
-// together; 1,021 BF16 tokens in blocks of 64 9.7 us and single tokens (254 4.5 us,
+// 25.7 us, 5.5 TB/s, of which 2 are the launch (issue 59% busy; BF16 rows 18.5);
+// 1,021 BF16 tokens in blocks of 64 9.7 us and single tokens (254 4.5 us,
 // 16 3.7 us) by the chain of slots, rows, earlier codes.
 #include <algorithm>
 #include <cstdint>
@@ -38,19 +38,21 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
-// CTAs of an SM, which say how many registers a thread has: four where FP32 prompts stream (three: 29.2 -> 30.3 us), else
-// three (four: single tokens of 254 requests 4.7 -> 5.4 us, 1,021 BF16 tokens in blocks of 64 10.5 -> 11.7).
-constexpr int append_ctas(bool f32, bool many) { return f32 && many ? 4 : 3; }
-constexpr int kQueryTokens = 2;        // tokens whose query rows a thread has in flight
+constexpr int kQueryTokens = 2;        // tokens whose query rows a thread has in flight, in registers
+constexpr int kStreamTokens = 4;       // and in shared memory
+// CTAs of an SM, which say how many registers a thread has, where a CTA of queries takes `tokens` of them: four where rows
+// stream (three: 4,000 FP32 tokens 25.5 -> 26.3 us, BF16 17.7 -> 18.8) and for 1,021 FP32 ones (8.4 -> 8.9, but 500 6.3 -> 5.6),
+// else three (four: single tokens of 254 requests 4.7 -> 5.4, 1,021 BF16 tokens 7.9 -> 8.8, in blocks of 64 9.8 -> 10.9).
+constexpr int append_ctas(bool f32, int tokens) {
+    return tokens == kStreamTokens || (f32 && tokens == kQueryTokens) ? 4 : 3;
+}
 constexpr int kMaxWindow = 32;         // tokens of a CTA that writes blocks
 constexpr int kMostShared = 8 * 8192 + (kMaxWindow - 1 + GEMV_MAX_BLOCK_TOKENS) * GEMV_MAX_HEAD_DIM / 2 * 8;   // bytes
 static_assert(kMaxWindow + GEMV_MAX_BLOCK_TOKENS <= 96 && kMaxWindow <= 32, "three ballots cover the tokens of a window");
 
-// How a launch is laid out: kv_ctas CTAs write blocks, each `every`-th of the first half or so (they wait for latencies
-// while the others stream: a FP32 prompt 29.4 us with all of them first, 28.2 so), the others turn queries.
+// How a launch is laid out: the first kv_ctas CTAs write blocks, the others turn queries.
 struct AppendShape {
     unsigned kv_ctas;
-    int every_shift;                   // log2 of `every`
     int window;                        // tokens of a CTA that writes blocks
     int kv_parts, kv_shift;            // CTAs that share a window's heads: the first half k's, the others v's
     int groups, across;                // of a head; tokens that a warp takes side by side
@@ -631,19 +633,102 @@ __device__ __forceinline__ void turn_queries(const RopeParams& p, const AppendSh
     }
 }
 
+// All but the last `left` groups of this thread's copies have landed. (A constant once the loop around it is unrolled.)
+__device__ __forceinline__ void wait_copies(int left) {
+    switch (left) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// The same of kStreamTokens tokens, whose rows come by asynchronous copies to places of a thread's own: more in flight, less
+// that begins and ends (4,054 tokens 29.3 -> 25.7 us; two tokens 26.9, eight 27.8).
+template <int VEC, bool F32>
+__device__ __forceinline__ void stream_queries(const RopeParams& p, const AppendShape& a, int64_t tok0, int part) {
+    constexpr int GAP = 2, es = F32 ? 4 : 2, TT = kStreamTokens;
+    extern __shared__ __align__(16) unsigned char s_rows[];
+    float2* const s_turn = reinterpret_cast<float2*>(s_rows + TT * kAppendThreads * 32);
+    const int groups = a.groups, half = p.rot_dim / 2, tid = threadIdx.x;
+    const int pitch = half / VEC * (VEC + GAP);
+    const int hy = groups == 1 ? tid : __umulhi(tid, a.per_group), gi = tid - hy * groups;
+    const int h = part * a.visit + hy;
+    const bool is_head = hy < a.visit && h < p.q_heads;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(TT), p.tokens - tok0));
+    const bool turned = gi * VEC < half;
+    const int c0 = turned && !p.interleaved ? gi * VEC : gi * 2 * VEC;
+    const int c1 = turned && !p.interleaved ? half + gi * VEC : gi * 2 * VEC + VEC;
+    unsigned char* const place = s_rows + tid * 16;
+    {
+        const char* row = static_cast<const char*>(p.q) + (tok0 * p.q_stride + h * p.head_dim) * es;
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            if (is_head && i < tokens) {
+                copy_async16(place + i * kAppendThreads * 32, row + c0 * es);
+                copy_async16(place + i * kAppendThreads * 32 + kAppendThreads * 16, row + c1 * es);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            row += p.q_stride * es;
+        }
+    }
+    const int lane = tid & 31;
+    const int slots = lane < tokens ? p.slots[tok0 + lane] : -1;
+    for (int i = tid; i < tokens * half; i += kAppendThreads) {
+        int t = 0, pair = i;
+#pragma unroll
+        for (int x = 1; x < TT; ++x)
+            if (pair >= half) {
+                pair -= half;
+                ++t;
+            }
+        const int axis = p.pair_axis ? min(max(p.pair_axis[pair], 0), p.axes - 1) : 0;
+        s_turn[t * pitch + pair + pair / VEC * GAP] = turn_of(p.positions[axis * p.axis_stride + tok0 + t], p.freqs[pair]);
+    }
+    __syncthreads();
+    uint16_t* o = p.q_out + tok0 * p.q_out_stride + h * p.head_dim;
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+        wait_copies(min(TT - 1 - i, 3));
+        const int slot = __shfl_sync(0xffffffffu, slots, i);
+        if (is_head && slot >= 0 && slot < p.num_slots) {            // else a padding row: nothing of it is written
+            Cols<VEC, F32> u, v;
+            u.load(reinterpret_cast<const char*>(place + i * kAppendThreads * 32), 0);
+            v.load(reinterpret_cast<const char*>(place + i * kAppendThreads * 32 + kAppendThreads * 16), 0);
+            float x[VEC], y[VEC];
+            u.values(x);
+            v.values(y);
+            if (turned) {
+                float cs[VEC], sn[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) {
+                    const float4 of = *reinterpret_cast<const float4*>(&s_turn[i * pitch + gi * (VEC + GAP) + j]);
+                    cs[j] = of.x; sn[j] = of.y; cs[j + 1] = of.z; sn[j + 1] = of.w;
+                }
+                turn_group<VEC>(x, y, p.interleaved, cs, sn);
+            }
+            store_bf16<VEC>(o, c0, x);
+            store_bf16<VEC>(o, c1, y);
+        }
+        o += p.q_out_stride;
+    }
+}
+
 template <int VEC, bool F32, int NI, int TT>
-__global__ void __launch_bounds__(kAppendThreads, append_ctas(F32, TT > 1))
+__global__ void __launch_bounds__(kAppendThreads, append_ctas(F32, TT))
 append_blocks_kernel(const __grid_constant__ RopeParams p, const __grid_constant__ BlockScales b,
                      const __grid_constant__ AppendShape a) {
     pdl_launch_dependents();
     pdl_wait_prerequisites();
-    const unsigned turn = blockIdx.x >> a.every_shift;
-    if (turn << a.every_shift == blockIdx.x && turn < a.kv_ctas) {
-        write_blocks<VEC, F32, NI>(p, b, a, static_cast<int>(turn));
+    if (blockIdx.x < a.kv_ctas) {
+        write_blocks<VEC, F32, NI>(p, b, a, static_cast<int>(blockIdx.x));
     } else {
-        const unsigned q = blockIdx.x - min(blockIdx.x + (1u << a.every_shift) - 1 >> a.every_shift, a.kv_ctas);
+        const unsigned q = blockIdx.x - a.kv_ctas;
         const unsigned at = a.parts_shift >= 0 ? q >> a.parts_shift : q / a.parts;
-        turn_queries<VEC, F32, TT>(p, a, static_cast<int64_t>(at) * TT, static_cast<int>(q - at * a.parts));
+        const int64_t tok0 = static_cast<int64_t>(at) * TT;
+        const int q_part = static_cast<int>(q - at * a.parts);
+        if constexpr (TT == kStreamTokens) stream_queries<VEC, F32>(p, a, tok0, q_part);
+        else turn_queries<VEC, F32, TT>(p, a, tok0, q_part);
     }
 }
 
@@ -653,8 +738,6 @@ cudaError_t launch_one(const RopeParams& p, const BlockScales& b, AppendShape a,
     const int64_t q = (static_cast<int64_t>(p.tokens) + TT - 1) / TT * a.parts;
     if (kv + q > 0x7fffffff) return cudaErrorInvalidConfiguration;
     a.kv_ctas = static_cast<unsigned>(kv);
-    a.every_shift = 0;
-    while (q >= (int64_t(2) << a.every_shift) * 2 * kv) ++a.every_shift;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(kv + q), 1, 1);
     cfg.blockDim = dim3(kAppendThreads, 1, 1);
@@ -694,22 +777,37 @@ cudaError_t launch_shape(const RopeParams& p, const BlockScales& b, int sm_count
     a.kv_shift = shift_of(a.kv_parts);
     // Windows as wide as it takes for one wave of CTAs, up to a block's tokens: a CTA without a run costs a microsecond
     // of its place, runs one after the other cost two each.
-    const bool many = static_cast<int64_t>(p.tokens) * a.parts >= 4 * sm_count;
-    const int64_t wave = static_cast<int64_t>(append_ctas(F32, many)) * sm_count;
+    // Queries by asynchronous copies where they are several waves of CTAs (us, registers -> so: 2,000 FP32 tokens of 32 heads
+    // of 128 15.8 -> 14.3, 4,000 BF16 ones 19.8 -> 17.7; 1,021 FP32 8.3 -> 8.7, 2,000 BF16 11.2 -> 11.5).
+    const int64_t queries = static_cast<int64_t>(p.tokens) * a.parts;
+    const int tokens = VEC > 1 && queries >= 20 * sm_count ? kStreamTokens : queries >= 4 * sm_count ? kQueryTokens : 1;
+    const int64_t wave = static_cast<int64_t>(append_ctas(F32, tokens)) * sm_count;
     const int64_t need = static_cast<int64_t>(p.tokens) * a.kv_parts;
     a.window = static_cast<int>(std::min<int64_t>({(need + wave - 1) / wave, std::max(b.tokens, 8), kMaxWindow}));
     a.turns = (a.window - 1 + b.tokens) * (p.rot_dim / 2);
     a.shared = kAppendWarps * NI * kLineBytes<VEC> + a.turns * 8;
-    return many ? launch_one<VEC, F32, NI, kQueryTokens>(p, b, a, s, pdl) : launch_one<VEC, F32, NI, 1>(p, b, a, s, pdl);
+    if constexpr (VEC > 1) {
+        if (tokens == kStreamTokens) {
+            a.shared = std::max(a.shared, kStreamTokens * (kAppendThreads * 32 + p.rot_dim / 2 / VEC * (VEC + 2) * 8));
+            return launch_one<VEC, F32, NI, kStreamTokens>(p, b, a, s, pdl);
+        }
+    }
+    return tokens > 1 ? launch_one<VEC, F32, NI, kQueryTokens>(p, b, a, s, pdl) : launch_one<VEC, F32, NI, 1>(p, b, a, s, pdl);
+}
+
+template <int VEC, bool F32, int NI, int TT>
+cudaError_t prepare_one() {
+    return cudaFuncSetAttribute(append_blocks_kernel<VEC, F32, NI, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMostShared);
 }
 
 template <int VEC, bool F32, int NI>
 cudaError_t prepare_shape() {
-    const cudaError_t e = cudaFuncSetAttribute(append_blocks_kernel<VEC, F32, NI, 1>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
-    return e == cudaSuccess ? cudaFuncSetAttribute(append_blocks_kernel<VEC, F32, NI, kQueryTokens>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared)
-                            : e;
+    cudaError_t e = prepare_one<VEC, F32, NI, 1>();
+    if (e == cudaSuccess) e = prepare_one<VEC, F32, NI, kQueryTokens>();
+    if constexpr (VEC > 1)
+        if (e == cudaSuccess) e = prepare_one<VEC, F32, NI, kStreamTokens>();
+    return e;
 }
 
 }  // namespace

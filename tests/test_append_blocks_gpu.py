@@ -136,6 +136,17 @@ def test_many_tokens(f32, requests, count, block):
     run_and_check(c, cache, slots)
 
 
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("q_heads,heads,dim,rot,axes,inter", [
+    (32, 2, 128, 128, 1, False), (20, 2, 256, 64, 3, False), (14, 1, 80, 80, 2, True), (64, 1, 16, 16, 1, False)])
+def test_prompts(f32, q_heads, heads, dim, rot, axes, inter):
+    """As many tokens as it takes for the queries to come by asynchronous copies; padding rows at odd places and at the end."""
+    held, new = [7, 0, 16], [(0, 7, 1101), None, (1, 0, 1300), None, None, None, (2, 16, 903), None, None]
+    cache = bc.BlockCache([h + n[2] for h, n in zip(held, [new[0], new[2], new[6]])], 32, 16, heads, dim, seed=dim, extra=16)
+    slots = tokens_of(cache, new)
+    run_and_check(Case(len(slots), q_heads, heads, dim, rot, axes, inter, f32, seed=8), cache, slots)
+
+
 def test_slots_past_the_pool_and_negative():
     cache = bc.BlockCache([40, 8], 16, 8, 2, 64, "token", seed=2)
     total = cache.num_pages * cache.page
