@@ -69,18 +69,23 @@ __global__ void __launch_bounds__(kReadThreads) cache_read_kernel(const __grid_c
     const int tid = threadIdx.x;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kReadRows;
 
-    // The request of row0: as many as end at it or before it.
-    int r = 0;
-    for (int i = 0; i < p.requests; i += kReadThreads) {
-        const bool past = i + tid < p.requests && p.row_start[i + tid + 1] <= row0;
-        const int n = __syncthreads_count(past);
-        r += n;
-        if (n < kReadThreads) break;
+    // The request of row0: as many as end at it or before it, searched kReadThreads at a time (one after the other: 4,096
+    // requests of 16 tokens 69.4 us, so 62.3, 65,536 of two 716 and 130).
+    int r = 0, step = 1;
+    while (static_cast<int64_t>(step) * kReadThreads < p.requests) step *= kReadThreads;
+    for (; step > 0; step /= kReadThreads) {
+        const int64_t i = r + static_cast<int64_t>(tid + 1) * step;
+        r += step * __syncthreads_count(i <= p.requests && p.row_start[i] <= row0);
     }
     if (tid < kReadRows) {
         const int64_t row = row0 + tid;
         int state = -1;
-        while (r < p.requests && p.row_start[r + 1] <= row) ++r;
+        // The row's own, a request or more on: steps that double, then halve.
+        auto past = [&](int64_t i) { return i <= p.requests && p.row_start[i] <= row; };
+        int64_t hop = 1;
+        for (; past(r + hop); hop *= 2) r += static_cast<int>(hop);
+        while ((hop /= 2) > 0)
+            if (past(r + hop)) r += static_cast<int>(hop);
         if (row < p.rows && r < p.requests) {
             const int64_t tok = (p.begin ? p.begin[r] : 0) + row - p.row_start[r];
             state = 0;

@@ -100,6 +100,38 @@ def test_many_requests():
     r.check()
 
 
+@pytest.mark.parametrize("requests", [255, 256, 257, 4096, 65536, 65537, 70001])
+def test_numbers_of_requests(requests):
+    """Numbers of requests on both sides of what one and two rounds of the search take; runs of requests without a row."""
+    g = torch.Generator().manual_seed(requests)
+    codes = torch.randint(0, 0x7F, (2, 512, 4, 1, 16), generator=g, dtype=torch.uint8).cuda()
+    scales = torch.exp2(torch.randint(-6, 7, (2, 512, 2), generator=g).float()).cuda()
+    table = torch.randint(0, 512, (requests, 1), generator=g, dtype=torch.int32).cuda()
+    begin = torch.randint(0, 3, (requests,), generator=g, dtype=torch.int32).cuda()
+    count = torch.randint(0, 3, (requests,), generator=g) * (torch.arange(requests) // 700 % 2)
+    start = torch.cat([torch.zeros(1, dtype=torch.int64), count.cumsum(0)])
+    rows = max(1, int(start[-1]))
+    out = [torch.full((rows, 16), MARK, device="cuda") for _ in range(2)]
+    cache = binding.kv_cache(codes[0], codes[1], kind=binding.GEMV_CACHE_FP8_BLOCK, num_pages=512, page_size=4, kv_heads=1,
+                             head_dim=16, page_stride=64, head_stride=16, slot_stride=16, block_tokens=2,
+                             k_block_scale=scales[0], v_block_scale=scales[1], scale_page_stride=2, scale_block_stride=1,
+                             scale_head_stride=1)
+    start_t = start.to(torch.int32).cuda()
+    binding.gemv_cache_read(binding.cache_read_args(
+        table=table, table_width=1, table_stride=1, begin=begin, row_start=start_t, requests=requests, rows=rows,
+        k_out=out[0], v_out=out[1], k_out_stride=16, v_out_stride=16, row_type=binding.GEMV_ROWS_F32), cache)
+    torch.cuda.synchronize()
+    of = torch.repeat_interleave(torch.arange(requests), count).cuda()
+    tok = begin[of] + torch.arange(len(of)).cuda() - start.cuda()[of]
+    ok = tok < 4                                   # (the others are past their row of the table: zeros, and the status bit)
+    page, tok = table[of, 0].long(), tok.clamp(max=3)
+    for i in range(2):
+        want = codes[i][page, tok, 0].view(torch.float8_e4m3fn).float() * scales[i][page, tok // 2, None]
+        want = torch.where(ok[:, None], want, torch.zeros_like(want))
+        assert torch.equal(out[i][:len(of)], want)
+    assert binding.gemv_device_status() == (0 if ok.all() else binding.GEMV_STATUS_BAD_PAGE)
+
+
 def test_fewer_rows_than_tokens():
     """No row past `rows` is written."""
     c = make("block", [50, 20], 16, 8, 4, 64)
