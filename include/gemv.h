@@ -800,8 +800,9 @@ int gemv_cache_read(const gemv_cache_read_args *args, const gemv_kv_cache *cache
  * by a power of two per head) are summed in FP32, the softmax is kept in FP32;
  * the probabilities, relative to the largest, meet V as two BF16 parts (2^-16;
  * FP8: as FP16, with 11 bits down to 2^-29 of the largest; with a scale for each
- * block the probabilities times v's scales, relative to the largest of those;
- * what is below 2^-126 of it counts as 0). requests = 0 is
+ * block the probabilities times v's scales, relative to the largest of those,
+ * while the sum of the probabilities themselves loses none above 2^-33 of the
+ * largest one, 2^-41 where v's scales are at most 2^120). requests = 0 is
  * allowed and does nothing. GEMV_ERR_UNSUPPORTED: more than 1,024 query heads
  * per key-value head; requests * kv_heads * (table_width * page_size / 16 + 2)
  * above 2,130,706,432.

@@ -23,12 +23,20 @@
 // factor. With a scale ks, vs for each block of tokens, a score is multiplied by
 // its token's ks, and with M the running maximum of s_j + log vs_j
 //
-//   w_j = exp(s_j + log vs_j - M),  out = sum_j w_j code_j / sum_j (w_j / vs_j):
+//   p_j = exp(s_j - M),  out = sum_j (p_j vs_j) code_j / sum_j p_j:
 //
-// one exponential and one maximum as before, and the weights, which meet the
-// codes in FP16, are relative to the largest of the products that are summed,
-// however far the scales of the blocks are apart. The scales of a slice's tokens
-// come by asynchronous copies beside its K, counted on the same barrier.
+// one exponential and one maximum as before, and the weights p_j vs_j, which
+// meet the codes in FP16, are relative to the largest of the products that are
+// summed, however far the scales of the blocks are apart. (The logarithm of vs
+// is in M alone, so its error divides out.) The sum of the p_j needs more of
+// FP32's range than the weights: with vs from 2^-60 to 2^128 the largest p_j is
+// between 2^-128 and 2^60 of a maximum of 1. So p_j is kept times 2^20 more
+// than the weights (2^31 tokens of 2^60 end below 2^127; what is lost is below
+// 2^-33 of the largest p_j, 2^-41 where scales are at most 2^120), and a sum
+// moves to another maximum by two factors, each the root of the whole, since
+// those of M's own distance may be below 2^-126 where the sum is not. The
+// scales of a slice's tokens come by asynchronous copies beside its K, counted on
+// the same barrier.
 //
 // Tiles. The group of query heads that share a key-value head are the narrow
 // side (N = 8) of the MMAs, 16 tokens of a slice (scores) or 16 columns of
@@ -278,7 +286,15 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     constexpr float kNegInf = -INFINITY;
     constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
     // Weights that meet V as FP16 are kept times 2^15 (the largest is 1): below 2^-14 FP16 has fewer bits.
-    constexpr float kUp = FP8 ? 15.f : 0.f, kDown = FP8 ? 0x1p-15f : 1.f;
+    constexpr float kUp = FP8 ? 15.f : 0.f;
+    // The weights' sum is kept times 2^20 more where a token's scale is not in it.
+    constexpr float kSumUp = BLOCK ? kUp + 20.f : kUp, kSumDown = BLOCK ? 0x1p-35f : FP8 ? 0x1p-15f : 1.f;
+    // A sum of weights whose maximum moves by 2^d (e: 2^d itself). FP32 holds the product also where it does not hold 2^d.
+    auto moved = [](float sum, float d, float e) {
+        if constexpr (!BLOCK) return sum * e;
+        const float root = exp2_ftz(0.5f * d);
+        return sum * root * root;
+    };
 
     // A piece of a row: slices s .. s + seg - 1 of ns, the first of them slice `at` of the CTA's range.
     struct Piece {
@@ -736,12 +752,12 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         else return make_uint2(*reinterpret_cast<const uint32_t*>(at + 4 * t),
                                *reinterpret_cast<const uint32_t*>(at + 16 + 4 * t));
     };
-    float v_scale = 1.f;
+    float v_scale = BLOCK ? 0x1p20f : 1.f;
     auto place_query = [&]() {
         ok = __all_sync(0xffffffffu, ok && wait_phase(smem_addr(&s_qbar[w]), q_phase)) != 0;
         q_phase ^= 1u;
         const float ksc = score_scale * (FP8 ? s_scales[w][0] : 1.f);
-        v_scale = FP8 ? s_scales[w][1] : 1.f;
+        if constexpr (FP8 && !BLOCK) v_scale = s_scales[w][1];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             col_scale[nb][0] = col_scale[nb][1] = ksc;
@@ -887,9 +903,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     }
                 }
             }
-            // Scales of the tokens of this lane's rows: of k, the logarithm of that of v, and one over it. From the
-            // logarithm, so that w / vs does not have its error.
-            float ks[BLOCK ? MT : 1][2], lv[BLOCK ? MT : 1][2], iv[BLOCK ? MT : 1][2];
+            // Scales of the tokens of this lane's rows: of k, the logarithm of that of v, and that of v itself by what the
+            // sum is kept larger.
+            float ks[BLOCK ? MT : 1][2], lv[BLOCK ? MT : 1][2], vs[BLOCK ? MT : 1][2];
             if constexpr (BLOCK) {
                 const float2* const at = reinterpret_cast<const float2*>(smem + S::kScalesAt + w * S::kScales) +
                                          (taken & (S::kScalePlaces - 1)) * TS;
@@ -898,9 +914,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float2 of = at[mt * 16 + j * 8 + g];
-                        ks[mt][j] = of.x;
-                        lv[mt][j] = log2_ftz(of.y < 0x1p-60f ? 0x1p-60f : of.y);
-                        iv[mt][j] = exp2_ftz(-lv[mt][j]);
+                        const float v_of = of.y < 0x1p-60f ? 0x1p-60f : of.y;
+                        ks[mt][j] = fmaf(of.y, 0.f, of.x);           // NaN where that of v is NaN, so that the sum is too
+                        lv[mt][j] = log2_ftz(v_of);
+                        vs[mt][j] = v_of * 0x1p-20f;
                     }
             }
             __syncwarp();
@@ -925,12 +942,6 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) x[mt][j] = cap_log2 * tanhf(x[mt][j]);
                 }
-                if constexpr (BLOCK) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) x[mt][j] += lv[mt][j >> 1];
-                }
                 if (valid != kAll) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
@@ -938,22 +949,29 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                         for (int j = 0; j < 4; ++j)
                             if (!(valid >> (mt * 16 + g + (j & 2) * 4) & 1u)) x[mt][j] = kNegInf;
                 }
-                float corr[2], base[2];
+                float corr[2], base[2], shift[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float top = fmaxf(x[0][j], x[0][j + 2]);
+                    auto term = [&](int mt, int i) {
+                        if constexpr (BLOCK) return x[mt][i] + lv[mt][i >> 1];
+                        else return x[mt][i];
+                    };
+                    float top = fmaxf(term(0, j), term(0, j + 2));
                     #pragma unroll
-                    for (int mt = 1; mt < MT; ++mt) top = fmaxf(top, fmaxf(x[mt][j], x[mt][j + 2]));
+                    for (int mt = 1; mt < MT; ++mt) top = fmaxf(top, fmaxf(term(mt, j), term(mt, j + 2)));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                     top = fmaxf(top, m[nb][j]);
                     base[j] = base_of(top);
-                    corr[j] = top == INFINITY ? 1.f : exp2_ftz(m[nb][j] - base[j]);   // this lane's l may be 0
+                    shift[j] = top == INFINITY ? 0.f : m[nb][j] - base[j];            // this lane's l may be 0
+                    corr[j] = exp2_ftz(shift[j]);
                     m[nb][j] = top;
                 }
-                l[nb][0] *= corr[0];
-                l[nb][1] *= corr[1];
+                if constexpr (!BLOCK) {
+                    l[nb][0] *= corr[0];
+                    l[nb][1] *= corr[1];
+                }
                 if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
@@ -962,17 +980,20 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                         acc[ks][nb][2] *= corr[0];
                         acc[ks][nb][3] *= corr[1];
                     }
+                    if constexpr (BLOCK) {
+                        l[nb][0] = moved(l[nb][0], shift[0], corr[0]);
+                        l[nb][1] = moved(l[nb][1], shift[1], corr[1]);
+                    }
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[mt][j] = exp2_ftz(x[mt][j] - (base[j & 1] - kUp));
+                    for (int j = 0; j < 4; ++j) x[mt][j] = exp2_ftz(x[mt][j] - (base[j & 1] - kSumUp));
+                    l[nb][0] += x[mt][0] + x[mt][2];
+                    l[nb][1] += x[mt][1] + x[mt][3];
                     if constexpr (BLOCK) {
-                        l[nb][0] += x[mt][0] * iv[mt][0] + x[mt][2] * iv[mt][1];
-                        l[nb][1] += x[mt][1] * iv[mt][0] + x[mt][3] * iv[mt][1];
-                    } else {
-                        l[nb][0] += x[mt][0] + x[mt][2];
-                        l[nb][1] += x[mt][1] + x[mt][3];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[mt][j] *= vs[mt][j >> 1];
                     }
                     // P as the B operand. FP16 beside an FP8 cache (2^-11 relative, down to 2^-29 of the largest
                     // weight). Beside a BF16 cache P has to be BF16, whose 2^-8 would double the rounding error of
@@ -1090,7 +1111,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                     // No weight: -inf. NaN scores, which no maximum shows, have made the sum NaN.
                     if (p.lse && g == 0 && hd < nh)
                         p.lse[static_cast<int64_t>(row) * p.q_heads + head_at + hd] =
-                            (m[nb][j] + log2f(l[nb][j] * kDown)) * kLn2;
+                            (m[nb][j] + log2f(l[nb][j] * kSumDown)) * kLn2;
                 }
                 // Transposed again, lane (g, t) holds columns 2t, 2t + 1 of the tile's rows for head g.
                 uint16_t* const o = p.out + static_cast<int64_t>(row) * p.out_stride + (head_at + nb * 8 + g) * p.head_dim;
@@ -1152,7 +1173,7 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
         *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * p.out_stride + head * p.head_dim + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (p.lse && d == 0)
-            p.lse[static_cast<int64_t>(row) * p.q_heads + head] = (top + log2f(sum * kDown)) * kLn2;
+            p.lse[static_cast<int64_t>(row) * p.q_heads + head] = (top + log2f(sum * kSumDown)) * kLn2;
     };
     const int d4s = p.head_dim / 4, items = nh * d4s;
     auto head_at = [&](int x) { return static_cast<int>(x * p.quarter_of >> 20); };   // x / d4s
@@ -1219,14 +1240,14 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
             }
             const float base = base_of(top);
             float e = exp2_ftz(ml_j.x - base);
-            float sum = ml_j.y * e;
+            float sum = moved(ml_j.y, ml_j.x - base, e);
             float4 o = make_float4(tail[u].x * e, tail[u].y * e, tail[u].z * e, tail[u].w * e);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
                 if (k < n - 1) {
                     const float4 v = *reinterpret_cast<const float4*>(smem + ((i >> 1) + k) * kAttnRing + place * 4);
                     e = exp2_ftz(ml[k].x - base);
-                    sum += ml[k].y * e;
+                    sum += moved(ml[k].y, ml[k].x - base, e);
                     o.x += v.x * e;
                     o.y += v.y * e;
                     o.z += v.z * e;
@@ -1320,13 +1341,13 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
                 for (int b = 0; b < B; ++b) next = fmaxf(next, ml[b][u].x);
                 const float base = base_of(next), e = exp2_ftz(top[u] - base);
-                sum[u] *= e;
+                sum[u] = moved(sum[u], top[u] - base, e);
                 o[u] = make_float4(o[u].x * e, o[u].y * e, o[u].z * e, o[u].w * e);
                 top[u] = next;
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     const float f = exp2_ftz(ml[b][u].x - base);
-                    sum[u] += ml[b][u].y * f;
+                    sum[u] += moved(ml[b][u].y, ml[b][u].x - base, f);
                     o[u].x += v[b][u].x * f;
                     o[u].y += v[b][u].y * f;
                     o[u].z += v[b][u].z * f;
@@ -1349,8 +1370,8 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
                 const float4 v = s_o[k * items + tid];
                 const float next = fmaxf(top[0], ml.x), base = base_of(next);
                 const float e = exp2_ftz(top[0] - base), f = exp2_ftz(ml.x - base);
+                sum[0] = moved(sum[0], top[0] - base, e) + moved(ml.y, ml.x - base, f);
                 top[0] = next;
-                sum[0] = sum[0] * e + ml.y * f;
                 o[0].x = o[0].x * e + v.x * f;
                 o[0].y = o[0].y * e + v.y * f;
                 o[0].z = o[0].z * e + v.z * f;
