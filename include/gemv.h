@@ -681,7 +681,9 @@ int gemv_block_tables(const gemv_block_tables_args *args, void *stream);
  * larger of need and the smallest power of two that is at least the old scale,
  * and where it grows the codes of the slots before the first new one become the
  * codes nearest to code * old scale / new scale (between powers of two exactly
- * the same values, but for those that fall among E4M3's subnormals). Slots
+ * the same values, but for those that fall among E4M3's subnormals). An old
+ * scale above 2^127 becomes 2^127, and the codes before the first new one
+ * code * old scale / 2^127, at most 448 in magnitude. Slots
  * behind the last new one keep their codes, whatever becomes of the scale. So
  * every scale that a call leaves in a block it writes to is a power of two. A
  * repeated call leaves the same bits.

@@ -174,13 +174,18 @@ __device__ __forceinline__ void store_codes(unsigned char* to, const float (&f)[
         *to = static_cast<unsigned char>(e4m3x2(x[0], 0.f));
 }
 
-// The smallest power of two that is at least `scale` (positive, normal).
+// The smallest power of two that is at least `scale` (positive, finite), 2^127 where there is none in FP32.
 __device__ __forceinline__ float power_above(float scale) {
     const uint32_t bits = __float_as_uint(scale);
-    return scale < 0x1p126f && (bits & 0x7fffffu) != 0u ? __uint_as_float((bits & 0x7f800000u) + 0x800000u) : scale;
+    const uint32_t up = (bits & 0x7fffffu) != 0u ? (bits & 0x7f800000u) + 0x800000u : bits;
+    return fminf(__uint_as_float(up), 0x1p127f);
 }
-// One over a power of two.
-__device__ __forceinline__ float one_over(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
+// One over a power of two from 2^-126 on. (That of 2^127 is subnormal.)
+__device__ __forceinline__ float one_over(float power) {
+    return power < 0x1p127f ? __uint_as_float((254u << 23) - __float_as_uint(power)) : 0x1p-127f;
+}
+// Whether the codes of a block move when its scale does: it grows, or comes down to the largest power of two.
+__device__ __forceinline__ bool scale_moves(float old, float scale) { return scale > old || old > 0x1p127f; }
 
 // The smallest power of two that is at least top / 448, no smaller than 2^-30; `top`: bits of a finite FP32 >= 0.
 __device__ __forceinline__ float scale_for(uint32_t top) {
@@ -303,8 +308,8 @@ __device__ __forceinline__ void write_singles(const RopeParams& p, const BlockSc
         const float need = scale_for(top);
         const float scale = held_run > 0 ? fmaxf(power_above(old), need) : need;
         const float inv = one_over(scale);
-        // Earlier tokens move to the new scale: the whole warp for each team whose scale grew.
-        const uint32_t grown = __ballot_sync(0xffffffffu, live && gi == 0 && held_run > 0 && scale > old);
+        // Earlier tokens move to the new scale: the whole warp for each team whose scale changes.
+        const uint32_t grown = __ballot_sync(0xffffffffu, live && gi == 0 && held_run > 0 && scale_moves(old, scale));
         for (uint32_t rest = grown; rest; rest &= rest - 1) {
             const int at = __ffs(rest) - 1;
             unsigned char* const block =
@@ -537,7 +542,7 @@ __device__ __forceinline__ void write_blocks(const RopeParams& p, const BlockSca
         const float scale = held_run > 0 ? fmaxf(power_above(old), need) : need;
         const float inv = one_over(scale);
         unsigned char* const block_at = (is_k ? p.kc : p.vc) + code_run + head * p.head_stride - held_run * p.slot_stride;
-        if (held_run > 0 && scale > old) {                           // earlier tokens move to the new scale
+        if (held_run > 0 && scale_moves(old, scale)) {               // earlier tokens move to the new scale
             move_block(block_at, p.slot_stride, held_run, p.head_dim, old * inv, rank * 32 + lane, 32 << team_shift);
         }
         if (rank == 0 && lane == 0 && scale != old) *scale_to = scale;   // (every lane has the old one)
