@@ -53,6 +53,7 @@ struct Workspace {
 struct DeviceState {
     bool ready = false;
     bool attn_ready = false;   // the attention kernels too: on the first attention call, which only they serve
+    bool attn_block_ready = false;   // those over a cache with scales for blocks: on the first such call
     bool cache_ready = false;  // and those of a cache with scales for blocks, and of reading a cache back, on theirs
     int status = GEMV_OK;
     int sm_count = 0;
@@ -637,15 +638,18 @@ namespace gemv {
 int api_device_state(int* sm_count) { return device_state(sm_count); }
 
 // The same, with the attention kernels' shared-memory limits raised. Setting them up with the GEMVs' would cost every
-// process 2.8 ms of its first GEMV call (4.2 -> 7.0 ms), and its failure that call.
-int api_attn_state(int* sm_count) {
+// process 2.8 ms of its first GEMV call (4.2 -> 7.0 ms), and its failure that call; those over a cache with scales for
+// blocks with the others' another 1.9 ms and 2 MB of the first attention call (3.2 -> 5.1 ms), and 20 us of every
+// gemv_device_status (102 -> 123).
+int api_attn_state(bool block, int* sm_count) {
     int rc = device_state(sm_count), dev = 0;
     if (rc != GEMV_OK) return rc;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
     std::lock_guard<std::mutex> lock(g_dev_mutex);
-    if (!g_dev[dev].attn_ready && (e = prepare_attn()) != cudaSuccess) return cuda_fail(e);
-    g_dev[dev].attn_ready = true;
+    bool& ready = block ? g_dev[dev].attn_block_ready : g_dev[dev].attn_ready;
+    if (!ready && (e = prepare_attn(block)) != cudaSuccess) return cuda_fail(e);
+    ready = true;
     return GEMV_OK;
 }
 
@@ -1209,16 +1213,17 @@ int gemv_device_status(unsigned int* bits, int reset) {
     if (!bits) return GEMV_ERR_INVALID;
     *bits = 0;
     // Each kernel translation unit keeps its own status word.
-    unsigned int b1 = 0, b2 = 0, b3 = 0, b4 = 0, b5 = 0, b6 = 0, b7 = 0;
+    unsigned int b1 = 0, b2 = 0, b3 = 0, b4 = 0, b5 = 0, b6 = 0, b7 = 0, b8 = 0;
     cudaError_t e = gemv::read_fma_status(&b1, reset != 0);
     if (e == cudaSuccess) e = gemv::read_mma_status_nb1(&b2, reset != 0);
     if (e == cudaSuccess) e = gemv::read_mma_status_nb2(&b3, reset != 0);
     if (e == cudaSuccess) e = gemv::read_fp8_status(&b4, reset != 0);
     if (e == cudaSuccess) e = gemv::read_tc_status(&b5, reset != 0);
-    if (e == cudaSuccess && in_use(&DeviceState::attn_ready)) e = gemv::read_attn_status(&b6, reset != 0);
+    if (e == cudaSuccess && in_use(&DeviceState::attn_ready)) e = gemv::read_attn_status(false, &b6, reset != 0);
+    if (e == cudaSuccess && in_use(&DeviceState::attn_block_ready)) e = gemv::read_attn_status(true, &b8, reset != 0);
     if (e == cudaSuccess && in_use(&DeviceState::cache_ready)) e = gemv::read_read_status(&b7, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e);
-    *bits = b1 | b2 | b3 | b4 | b5 | b6 | b7;
+    *bits = b1 | b2 | b3 | b4 | b5 | b6 | b7 | b8;
     return GEMV_OK;
 }
 

@@ -62,10 +62,14 @@ cudaError_t launch_attn(const AttnParams& p, const AttnLaunch& l, cudaStream_t s
     return attn_launch_bf16_256(p, l, s, pdl);
 }
 
-cudaError_t prepare_attn() {
+cudaError_t prepare_attn(bool block) {
+    if (block) {
+        cudaError_t e = attn_prepare_fp8b_64();
+        if (e == cudaSuccess) e = attn_prepare_fp8b_128();
+        return e == cudaSuccess ? attn_prepare_fp8b_256() : e;
+    }
     cudaError_t (*const all[])() = {attn_prepare_bf16_64, attn_prepare_bf16_128, attn_prepare_bf16_256,
-                                    attn_prepare_fp8_64, attn_prepare_fp8_128, attn_prepare_fp8_256,
-                                    attn_prepare_fp8b_64, attn_prepare_fp8b_128, attn_prepare_fp8b_256};
+                                    attn_prepare_fp8_64, attn_prepare_fp8_128, attn_prepare_fp8_256};
     for (auto f : all) {
         const cudaError_t e = f();
         if (e != cudaSuccess) return e;
@@ -73,16 +77,16 @@ cudaError_t prepare_attn() {
     return cudaSuccess;
 }
 
-cudaError_t read_attn_status(unsigned int* bits, bool reset) {
-    cudaError_t (*const all[])(unsigned int*, bool) = {attn_status_bf16_64, attn_status_bf16_128,
-                                                       attn_status_bf16_256, attn_status_fp8_64,
-                                                       attn_status_fp8_128, attn_status_fp8_256,
-                                                       attn_status_fp8b_64, attn_status_fp8b_128,
-                                                       attn_status_fp8b_256};
+cudaError_t read_attn_status(bool block, unsigned int* bits, bool reset) {
+    using Status = cudaError_t (*)(unsigned int*, bool);
+    static constexpr Status of_blocks[] = {attn_status_fp8b_64, attn_status_fp8b_128, attn_status_fp8b_256};
+    static constexpr Status others[] = {attn_status_bf16_64, attn_status_bf16_128, attn_status_bf16_256,
+                                        attn_status_fp8_64, attn_status_fp8_128, attn_status_fp8_256};
+    const Status* const all = block ? of_blocks : others;
     *bits = 0;
-    for (auto f : all) {
+    for (int i = 0; i < (block ? 3 : 6); ++i) {
         unsigned int b = 0;
-        const cudaError_t e = f(&b, reset);
+        const cudaError_t e = all[i](&b, reset);
         if (e != cudaSuccess) return e;
         *bits |= b;
     }

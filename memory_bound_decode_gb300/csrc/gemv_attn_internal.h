@@ -12,7 +12,7 @@ namespace gemv {
 
 // ---- shared with gemv_api.cpp -------------------------------------------------
 int api_device_state(int* sm_count);      // set-up of the current device; GEMV_OK or an error
-int api_attn_state(int* sm_count);        // and of its attention kernels
+int api_attn_state(bool block, int* sm_count);   // and of its attention kernels; block: with a scale for each block
 int api_cache_state(int* sm_count);       // or of those that write a cache with scales for blocks and read a cache back
 int api_cuda_fail(cudaError_t e);         // record e for gemv_last_cuda_error; GEMV_ERR_CUDA
 bool api_pdl_enabled();
@@ -100,8 +100,8 @@ struct AttnLaunch {
 int plan_attn(int q_heads, int kv_heads, int head_dim, int kind, int sm_count, AttnLaunch* l);   // kind: GEMV_CACHE_*
 
 cudaError_t launch_attn(const AttnParams& p, const AttnLaunch& l, cudaStream_t s, bool pdl);
-cudaError_t prepare_attn();
-cudaError_t read_attn_status(unsigned int* bits, bool reset);
+cudaError_t prepare_attn(bool block);     // the kernels over a cache with a scale for each block, or the others
+cudaError_t read_attn_status(bool block, unsigned int* bits, bool reset);
 
 // ---- rotary positions -----------------------------------------------------------
 
