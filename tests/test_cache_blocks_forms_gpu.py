@@ -7,6 +7,7 @@ from tests import attn_util as au
 from tests import blocks_cache as bc
 from tests.test_append_blocks_gpu import check, same_bits
 from tests.test_attn_blocks_gpu import Attn
+from tests.test_cache_read_gpu import Read
 from tests.test_rope_gpu import Case
 
 pytestmark = pytest.mark.gpu
@@ -114,4 +115,33 @@ def test_calls_at_the_same_time():
             run(b, s.cuda_stream)
         for x, y in zip(alone, results()):
             assert same_bits(x, y)
+    assert binding.gemv_device_status() == 0
+
+
+@pytest.mark.parametrize("requests", [2, 3, 4, 8, 9, 10])
+@pytest.mark.parametrize("length", [512, 513, 600, 1024, 1025])
+def test_rows_of_one_length(requests, length):
+    """Attention on both sides of the lengths and numbers of rows that are cut between CTAs."""
+    cache = bc.BlockCache([length] * requests, 64, 32, 8, 64, "head", seed=length)
+    a = Attn(cache=cache, lens=[length] * requests, q_heads=8, seed=3)
+    for _ in range(2):
+        a.guard.fill_(-777.0)
+        a.run()
+        torch.cuda.synchronize()
+        a.check()
+
+
+@pytest.mark.parametrize("row_type", ["bf16", "f32"])
+@pytest.mark.parametrize("given", [(True, True), (False, False), (True, False), (False, True)])
+def test_read_without_scales(row_type, given):
+    """Rows of an FP8 cache whose scales per head are left out: 1."""
+    c = au.Cache([70, 5], 16, 3, 80, "fp8", "token", seed=4)
+    for i in range(2):
+        if not given[i]:
+            c.values[i] = [v / c.scales[i].double().cpu()[:, None] for v in c.values[i]]
+            c.values[i] = [v.float().to(torch.float8_e4m3fn).double() for v in c.values[i]]      # the codes, as they are
+            c.scales[i] = None
+    r = Read(c, [3, 0], [67, 5], row_type, pad=8, behind=2)
+    r.run()
+    r.check()
     assert binding.gemv_device_status() == 0
