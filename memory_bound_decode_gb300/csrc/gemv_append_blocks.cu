@@ -19,10 +19,12 @@
 // once, and what is in flight takes no registers. Single tokens (a decode step)
 // take the lanes that hold a row, and registers.
 //
-// Measured: 4,054 tokens of 32 + 8 + 8 FP32 heads of 128 in blocks of 16 (141 MB)
-// 25.7 us, 5.5 TB/s, of which 2 are the launch (issue 59% busy; BF16 rows 18.5);
-// 1,021 BF16 tokens in blocks of 64 9.7 us and single tokens (254 4.5 us,
-// 16 3.7 us) by the chain of slots, rows, earlier codes.
+// Measured: 4,051 tokens (4,084 rows) of 32 + 8 + 8 FP32 heads of 128 in blocks of
+// 16 (141 MB) 25.7 us, 5.5 TB/s, of which 2 are the launch (issue 59% busy; BF16
+// rows 18.5); 1,021 BF16 tokens in blocks of 64 9.7 us. Single tokens, in a
+// replayed graph: 16 2.5 us, 254 4.8 us where no scale grows (launch, then slots
+// and rows one after the other), 5.3 and 12.2 us where a quarter of the blocks
+// do, 5.6 and 15.2 us where all do (then the codes of their earlier tokens).
 #include <algorithm>
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -649,7 +651,7 @@ __device__ __forceinline__ void wait_copies(int left) {
 }
 
 // The same of kStreamTokens tokens, whose rows come by asynchronous copies to places of a thread's own: more in flight, less
-// that begins and ends (4,054 tokens 29.3 -> 25.7 us; two tokens 26.9, eight 27.8).
+// that begins and ends (4,051 tokens 29.3 -> 25.7 us; two tokens 26.9, eight 27.8).
 template <int VEC, bool F32>
 __device__ __forceinline__ void stream_queries(const RopeParams& p, const AppendShape& a, int64_t tok0, int part) {
     constexpr int GAP = 2, es = F32 ? 4 : 2, TT = kStreamTokens;

@@ -421,7 +421,10 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     // With a scale for each block a CTA takes the rows of up to two slices per warp that begin in its range, whole, and
     // longer ones are cut evenly (us, ranges that cut rows of any length -> so: 16 requests of 0 to 128 tokens
     // 10.6 -> 7.8, to 1,024 14.6 -> 12.0, to 2,048 19.5 -> 15.8, 13 of 1 to 2,000 20.1 -> 15.2; whole rows of up to four
-    // slices per warp 17.5 and 16.1 in the last two).
+    // slices per warp 17.5 and 16.1 in the last two). With more requests than threads rows are cut as they come; ranges
+    // long enough to cut few of them, as for the other kinds, took as long (400 requests of 0 to 64 tokens 21.9 and 22.0,
+    // to 300 41.4 and 41.5, to 1,024 82.6 and 82.6). Rows of one length go by the rule below, whole or cut: 8 KV heads,
+    // cut -> whole, 1 x 1,000 9.4 -> 9.9, 2 9.8 -> 10.0, 8 10.3 -> 10.2; 2 x 600 9.7 -> 9.6, 4 10.0 -> 9.8, 8 10.2 -> 9.9.
     const bool whole_rows = BLOCK && longest <= 2 * W && p.requests <= T;
     const bool uncut = !BLOCK && (longest <= 2 * W || (longest <= 4 * W && even * 4 >= longest));
     int quota = whole_rows ? even : max(even, max(W, uncut ? longest : 0));

@@ -4,7 +4,7 @@
 //
 // One pass: codes in, rows out, bound by HBM: 16 requests of up to 4,096 tokens
 // (8 heads of 128 to BF16 rows, 201 MB) 32.3 us, 6.2 TB/s; FP32 rows of 840 MB
-// in all 129 us, 6.5 TB/s; 300 tokens 3.6 us, of which 2 are the launch.
+// in all 129 us, 6.5 TB/s; 300 tokens 3.2 us in a replayed graph, of which 2 are the launch.
 // A CTA takes kReadRows rows (4, 8, 16, 32: 35.6, 34.0, 34.8, 35.8 us): it
 // finds the request of the first among row_start, its threads the pages of one
 // row each, then every thread brings the same 16 bytes of row after row.
