@@ -33,10 +33,9 @@
 // between 2^-128 and 2^60 of a maximum of 1. So p_j is kept times 2^20 more
 // than the weights (2^31 tokens of 2^60 end below 2^127; what is lost is below
 // 2^-33 of the largest p_j, 2^-41 where scales are at most 2^120), and a sum
-// moves to another maximum by two factors, each the root of the whole, since
-// those of M's own distance may be below 2^-126 where the sum is not. The
-// scales of a slice's tokens come by asynchronous copies beside its K, counted on
-// the same barrier.
+// moves to another maximum by the root of the factor, twice: the factor may be
+// below 2^-126 where the product is not. The scales of a slice's tokens come by
+// asynchronous copies beside its K, counted on the same barrier.
 //
 // Tiles. The group of query heads that share a key-value head are the narrow
 // side (N = 8) of the MMAs, 16 tokens of a slice (scores) or 16 columns of
@@ -287,9 +286,9 @@ attn_decode_kernel(const __grid_constant__ AttnParams p) {
     constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
     // Weights that meet V as FP16 are kept times 2^15 (the largest is 1): below 2^-14 FP16 has fewer bits.
     constexpr float kUp = FP8 ? 15.f : 0.f;
-    // The weights' sum is kept times 2^20 more where a token's scale is not in it.
+    // A sum without the scales of v, which those of blocks are not in, is kept times 2^20 more.
     constexpr float kSumUp = BLOCK ? kUp + 20.f : kUp, kSumDown = BLOCK ? 0x1p-35f : FP8 ? 0x1p-15f : 1.f;
-    // A sum of weights whose maximum moves by 2^d (e: 2^d itself). FP32 holds the product also where it does not hold 2^d.
+    // Such a sum where the maximum moves: times 2^d (e: 2^d itself, which may be too small for FP32 where the product is not).
     auto moved = [](float sum, float d, float e) {
         if constexpr (!BLOCK) return sum * e;
         const float root = exp2_ftz(0.5f * d);
